@@ -72,7 +72,8 @@ typedef enum {
     KVPACK_ERR_WORKSPACE = 4,     /* workspace pointer null or smaller than the query says */
     KVPACK_ERR_CUDA = 5,          /* a CUDA runtime call failed (launch, attribute, ...) */
     KVPACK_ERR_NOCONVERGE = 6,    /* device: eigen-solver hit its iteration cap */
-    KVPACK_ERR_TIMEOUT = 7        /* device: a bounded wait expired */
+    KVPACK_ERR_TIMEOUT = 7,       /* device: a bounded wait expired */
+    KVPACK_ERR_PAGE = 8           /* device: a sequence length or block-table entry out of range */
 } kvpack_status;
 
 /*
@@ -310,6 +311,129 @@ kvpack_status kvpack_decompress(const kvpack_dims *dims, int32_t n_layers,
                                 const uint16_t *CK_lo, const uint16_t *CK_hi, const uint16_t *BK,
                                 const uint16_t *CV_lo, const uint16_t *CV_hi, const uint16_t *BV,
                                 const uint32_t *mask, uint16_t *K_out, uint16_t *V_out, int32_t L_cap, void *stream);
+
+/* ------------------------------------------------------------ rotary positions
+ * Positions of images and video have several axes (time, height, width), and each
+ * pair of a head's entries turns by one of them.  freq[p] (fp64, device) is the angle
+ * per position step of pair p, axis[p] < n_axes its axis; with R = rotary_dim and
+ * p < R / 2, for every head x of 128 values of a row:
+ *   t = pos[axis[p]][row] * freq[p]
+ *   (x[p], x[p + R/2])  or, adjacent,  (x[2p], x[2p + 1])
+ *        <-  (a cos t - b sin t, b cos t + a sin t)
+ * and x[R ..] passes unchanged.  The angle is reduced in fp64, so that far positions
+ * keep their precision; the rotation is fp32, rounded once to bf16.
+ * Supported: R a multiple of 16 up to 128, n_axes 1 .. 4.
+ *
+ * kvpack_heads names heads of 128 bf16 values: head h of row r of outer row o starts at
+ *   data + o * outer_stride + r * row_stride + (h / 4) * group_stride + (h % 4) * 128
+ * elements.  Heads side by side have group_stride 512, so q, k and v may be slices of one
+ * projection's output; group_stride T * 512, row_stride 512 is the compression's input X
+ * [units][T][512].  data must be 16-byte aligned, the strides multiples of 8.
+ *
+ * kvpack_rope -- rotates n_q heads of q and n_k heads of k (either count may be 0, its
+ * pointers are then not read) in n_outer x n_rows rows; pos [n_axes][n_outer][n_rows].
+ * inverse != 0 turns back (by -t), which is also the gradient of the rotation.  An output
+ * may be its input (same data and strides); otherwise outputs overlap nothing.
+ * n_rows = 0 launches nothing.
+ */
+#define KVPACK_MAX_AXES 4
+
+typedef struct kvpack_heads {
+    uint16_t *data;
+    int64_t outer_stride, row_stride, group_stride;
+} kvpack_heads;
+
+typedef struct kvpack_rope_spec {
+    int32_t rotary_dim;           /* R */
+    int32_t n_axes;
+    int32_t adjacent;             /* 0: pairs (p, p + R/2), 1: pairs (2p, 2p + 1) */
+    uint8_t axis[64];             /* of each pair p < R / 2 */
+} kvpack_rope_spec;
+
+kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, const int32_t *pos,
+                          int32_t n_outer, int32_t n_rows,
+                          int32_t n_q, const kvpack_heads *q, const kvpack_heads *q_out,
+                          int32_t n_k, const kvpack_heads *k, const kvpack_heads *k_out,
+                          int32_t inverse, void *stream);
+
+/* ----------------------------------------------------------------- paged cache
+ * An uncompressed bf16 cache whose sequences have lengths of their own:
+ *   K_pages, V_pages  [n_layers][n_pages][n_kv_heads][page_size][128]
+ *   block_table       [batch][max_pages] int32: token i of sequence b lies in page
+ *                     block_table[b][i / page_size], row i % page_size (all layers alike)
+ *   seq_lens          [batch] int32, 0 .. max_pages * page_size
+ * Table entries behind a sequence's last page are not read.  Sequences may share pages
+ * that none of them appends to.  Lengths and tables are read on the device, so a captured
+ * graph may be replayed after they have changed.  A length or a page number out of range
+ * is reported as KVPACK_ERR_PAGE by kvpack_last_device_status(); nothing outside the
+ * pools is touched, but that call's results are not to be used.
+ * Supported: head_dim 128, n_q_heads a multiple of n_kv_heads with a ratio up to 8,
+ * n_kv_heads <= 1024, page_size a power of two 16 .. 256, batch <= KVPACK_MAX_PAGED_BATCH,
+ * max_pages * page_size <= KVPACK_MAX_PAGED_TOKENS.
+ *
+ * kvpack_paged_append -- the new tokens' keys, rotated, and values into their pages, and
+ * the queries rotated into q_out.  Outer rows of q, k, v, q_out are the n_layers layers.
+ * seq_lens counts the new tokens already.  Row r belongs to sequence b with
+ * row_offsets[b] <= r < row_offsets[b + 1] (int32 [batch + 1], ascending, row_offsets[0]
+ * = 0) and is its token seq_lens[b] - row_offsets[b + 1] + r; rows from
+ * row_offsets[batch] on belong to none and are left as they are.  row_offsets NULL: one
+ * row per sequence (n_rows = batch), its token seq_lens[b] - 1; a sequence of length 0
+ * then has none.  pos [n_axes][n_rows].  spec NULL: nothing is rotated (freq and pos are
+ * not read).  q and q_out may both be NULL; q_out may be q.
+ *
+ * kvpack_paged_decode_attn -- attention of one query per sequence, for each layer and
+ * query head h (KV head j = h / (n_q / n_kv)):
+ *   s_t = softmax_scale * q_h . K_t[j],  t < seq_lens[b]
+ *   out_h = sum_t softmax(s)_t V_t[j],   lse_h = ln sum_t exp(s_t)
+ * q, out [n_layers * batch][n_q_heads][128]; lse [n_layers * batch][n_q_heads] fp32 or
+ * NULL.  A sequence of length 0 gets out = 0 and lse = -inf.  Accumulation is fp32; the
+ * work split depends on the shapes and lengths alone, so repeated calls give identical
+ * bits.  ws must hold kvpack_paged_decode_workspace(dims, n_layers) bytes; calls that may
+ * run at the same time need one each.
+ *
+ * kvpack_decode_attn_paged -- kvpack_decode_attn with the text tail in a paged cache, of
+ * seq_lens[b] tokens in batch row b (0 for none): one softmax over the T visual tokens and
+ * those.  batch, n_q_heads and n_kv_heads of both shapes must agree; dims->L_text_cap is
+ * not used.  ws must hold kvpack_decode_paged_workspace(dims, pdims, n_layers) bytes.
+ */
+#define KVPACK_MAX_PAGED_BATCH 4096
+#define KVPACK_MAX_PAGED_TOKENS (1 << 24)
+
+typedef struct kvpack_paged_dims {
+    int32_t batch;
+    int32_t n_q_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t n_pages;
+    int32_t max_pages;
+} kvpack_paged_dims;
+
+kvpack_status kvpack_paged_append(const kvpack_paged_dims *dims, int32_t n_layers,
+                                  const kvpack_rope_spec *spec, const double *freq, const int32_t *pos,
+                                  int32_t n_rows, const kvpack_heads *q, const kvpack_heads *k,
+                                  const kvpack_heads *v, const int32_t *row_offsets,
+                                  const int32_t *seq_lens, const int32_t *block_table,
+                                  const kvpack_heads *q_out, uint16_t *K_pages, uint16_t *V_pages,
+                                  void *stream);
+
+size_t kvpack_paged_decode_workspace(const kvpack_paged_dims *dims, int32_t n_layers);
+kvpack_status kvpack_paged_decode_attn(const kvpack_paged_dims *dims, int32_t n_layers, const uint16_t *q,
+                                       const uint16_t *K_pages, const uint16_t *V_pages,
+                                       const int32_t *block_table, const int32_t *seq_lens,
+                                       float softmax_scale, uint16_t *out, float *lse,
+                                       void *ws, size_t ws_bytes, void *stream);
+
+size_t kvpack_decode_paged_workspace(const kvpack_dims *dims, const kvpack_paged_dims *pdims, int32_t n_layers);
+kvpack_status kvpack_decode_attn_paged(const kvpack_dims *dims, const kvpack_paged_dims *pdims, int32_t n_layers,
+                                       const uint16_t *q,
+                                       const uint16_t *CK_lo, const uint16_t *CK_hi, const uint16_t *BK,
+                                       const uint16_t *CV_lo, const uint16_t *CV_hi, const uint16_t *BV,
+                                       const uint16_t *K_pages, const uint16_t *V_pages,
+                                       const int32_t *block_table, const int32_t *seq_lens,
+                                       const uint32_t *mask, float softmax_scale,
+                                       uint16_t *out, float *mass,
+                                       void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ helpers */
 

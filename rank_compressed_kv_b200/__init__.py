@@ -18,6 +18,12 @@ Functions mirror the C entry points:
     decode_attn_q4(dims, n_layers, q, QK_lo, QK_hi, EK, BK, QV_lo, QV_hi, EV, BV,
                    K_text, V_text, L_text, mask, scale, out, mass, ws)
     select(dims, n_layers, mass, score, alpha, k_hi, mask_out)
+    rope(spec, freq, pos, q, q_out, k, k_out, inverse)
+    paged_append(dims, n_layers, spec, freq, pos, q, k, v, row_offsets, seq_lens, block_table,
+                 q_out, K_pages, V_pages)
+    paged_decode_attn(dims, n_layers, q, K_pages, V_pages, block_table, seq_lens, scale, out, lse, ws)
+    decode_attn_paged(dims, pdims, n_layers, q, CK_lo, CK_hi, BK, CV_lo, CV_hi, BV, K_pages, V_pages,
+                      block_table, seq_lens, mask, scale, out, mass, ws)
 
 bf16 arrays are torch.bfloat16 (or int16 views of bf16 bits); masks are
 torch.int32 holding the uint32 words; fp32 arrays are torch.float32.
@@ -25,11 +31,15 @@ torch.int32 holding the uint32 words; fp32 arrays are torch.float32.
 from ._lib import (  # noqa: F401
     Dims,
     KvpackError,
+    PagedDims,
+    Rope,
     STATUS_NAMES,
     compress,
     compress_workspace,
     decode_attn,
     decode_attn_noalloc,
+    decode_attn_paged,
+    decode_paged_workspace,
     decode_attn_tb,
     decode_tb_workspace,
     decode_attn_q4,
@@ -43,6 +53,10 @@ from ._lib import (  # noqa: F401
     last_device_status,
     lib,
     library_path,
+    paged_append,
+    paged_decode_attn,
+    paged_decode_workspace,
+    rope,
     select,
     selftest_bounded_wait,
     version,

@@ -1,7 +1,7 @@
 // kvpack.cu -- the C ABI of libkvpack (see include/kvpack.h): argument
 // validation, workspace planning and kernel launches.  Everything that
-// computes runs in the kernels of decode.cuh, rstream.cuh, select.cuh and
-// compress.cuh.
+// computes runs in the kernels of decode.cuh, rstream.cuh, select.cuh,
+// compress.cuh, rope.cuh and paged.cuh.
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -18,6 +18,8 @@
 #include "baseline.cuh"
 #include "select.cuh"
 #include "compress.cuh"
+#include "rope.cuh"
+#include "paged.cuh"
 
 namespace {
 
@@ -74,7 +76,7 @@ inline int round_heads(int Hg) { return Hg <= 4 ? 4 : Hg <= 8 ? 8 : Hg <= 16 ? 1
 // Most partial slots any unit gets when NT tiles are split over C CTAs (tpu tiles per unit).
 inline int max_slots(long long NT, long long C, int tpu) { return (int)(((long long)tpu * C + NT - 1) / NT) + 1; }
 
-DecodePlan plan_decode(const kvpack_dims *d, int32_t n_layers, int L_c = 0) {
+DecodePlan plan_decode(const kvpack_dims *d, int32_t n_layers, int L_c = 0, bool paged_text = false) {
     DecodePlan pl{};
     pl.Hg = hg(d);
     pl.NH = round_heads(pl.Hg);
@@ -88,7 +90,7 @@ DecodePlan plan_decode(const kvpack_dims *d, int32_t n_layers, int L_c = 0) {
     pl.cta_v = pl.cta_s;
     pl.nslot_s = max_slots(pl.ntiles, pl.cta_s, pl.tpu);
     pl.nslot_v = max_slots(pl.ntiles, pl.cta_v, pl.tpu);
-    pl.Sc_max = (d->L_text_cap + kTextChunk - 1) / kTextChunk;
+    pl.Sc_max = paged_text ? 1 : (d->L_text_cap + kTextChunk - 1) / kTextChunk;   // paged: joined to one partial
     size_t off = 0;
     pl.off_qt = off;
     off = align256(off + (size_t)pl.units * kvpack::decode::qblock_bytes(pl.Hg));
@@ -343,6 +345,7 @@ const char *kvpack_status_string(kvpack_status s) {
         case KVPACK_ERR_CUDA: return "KVPACK_ERR_CUDA";
         case KVPACK_ERR_NOCONVERGE: return "KVPACK_ERR_NOCONVERGE";
         case KVPACK_ERR_TIMEOUT: return "KVPACK_ERR_TIMEOUT";
+        case KVPACK_ERR_PAGE: return "KVPACK_ERR_PAGE";
     }
     return "KVPACK_ERR_UNKNOWN";
 }
@@ -378,21 +381,118 @@ size_t kvpack_decode_workspace(const kvpack_dims *d, int32_t n_layers) {
 
 namespace {
 
+// ------------------------------------------------------------------ paged cache
+
+namespace pg = kvpack::paged;
+
+kvpack_status check_paged(const kvpack_paged_dims *d, int32_t n_layers) {
+    if (d == nullptr || n_layers <= 0) return KVPACK_ERR_INVALID_ARG;
+    if (d->batch <= 0 || d->n_q_heads <= 0 || d->n_kv_heads <= 0 || d->page_size <= 0 || d->n_pages <= 0 ||
+        d->max_pages <= 0)
+        return KVPACK_ERR_INVALID_ARG;
+    if (d->head_dim != KVPACK_HEAD_DIM || d->n_q_heads % d->n_kv_heads != 0) return KVPACK_ERR_UNSUPPORTED;
+    if (d->n_q_heads / d->n_kv_heads > 8 || d->n_kv_heads > 1024) return KVPACK_ERR_UNSUPPORTED;
+    if (d->batch > KVPACK_MAX_PAGED_BATCH) return KVPACK_ERR_UNSUPPORTED;
+    if (d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
+        return KVPACK_ERR_UNSUPPORTED;
+    if ((long long)d->max_pages * d->page_size > KVPACK_MAX_PAGED_TOKENS) return KVPACK_ERR_UNSUPPORTED;
+    if ((long long)n_layers * d->batch * d->n_q_heads > (1LL << 30)) return KVPACK_ERR_UNSUPPORTED;
+    return KVPACK_OK;
+}
+
+inline int log2_exact(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+struct PagedPlan {
+    long long units;
+    int per_kv, grid;
+    size_t off_stat, off_acc, off_desc, total;
+};
+
+// One wave of a full B200, fewer blocks where the tables' capacity cannot give every warp a run.
+PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
+    PagedPlan pl{};
+    pl.units = (long long)n_layers * d->batch * d->n_kv_heads;
+    pl.per_kv = d->n_q_heads / d->n_kv_heads;
+    const long long tiles = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile);
+    const long long blocks = (tiles + pg::kMinTiles - 1) / pg::kMinTiles;   // runs; one per block, at first
+    pl.grid = (int)(blocks < kPlanSMs * pg::kBlocksPerSM ? blocks : kPlanSMs * pg::kBlocksPerSM);
+    const size_t slots = 2 * (size_t)pl.grid * pg::kWarps;
+    size_t off = 0;
+    pl.off_stat = off;
+    off = align256(off + slots * 8 * 2 * sizeof(float));
+    pl.off_acc = off;
+    off = align256(off + slots * pl.per_kv * 128 * sizeof(float));
+    pl.off_desc = off;
+    off = align256(off + (size_t)pl.units * sizeof(int2));
+    pl.total = off;
+    return pl;
+}
+
+// out and lse of every unit, or (out null) the softmax parts of every query head in the text tail's
+// partial layout
+kvpack_status launch_paged_attend(const kvpack_paged_dims *d, int32_t n_layers, const uint16_t *q, const uint16_t *K,
+                                  const uint16_t *V, const int32_t *table, const int32_t *lens, float softmax_scale,
+                                  uint16_t *out, float *lse, float *tpart, void *ws, cudaStream_t st) {
+    const PagedPlan pl = plan_paged(d, n_layers);
+    unsigned char *w = static_cast<unsigned char *>(ws);
+    pg::Params p{};
+    p.q = q; p.K = K; p.V = V; p.table = table; p.lens = lens; p.out = out; p.lse = lse; p.tpart = tpart;
+    p.stat = reinterpret_cast<float *>(w + pl.off_stat);
+    p.acc = reinterpret_cast<float *>(w + pl.off_acc);
+    p.desc = reinterpret_cast<int2 *>(w + pl.off_desc);
+    p.layers = n_layers; p.batch = d->batch; p.n_kv = d->n_kv_heads; p.per_kv = pl.per_kv;
+    p.n_pages = d->n_pages; p.max_pages = d->max_pages; p.page_shift = log2_exact(d->page_size);
+    p.warps = pl.grid * pg::kWarps;
+    p.scale2 = softmax_scale * 1.4426950408889634f;
+    pg::attend_kernel<<<pl.grid, pg::kThreads, (d->batch + 1) * sizeof(long long), st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return KVPACK_ERR_CUDA;
+    return launch_pdl(pg::join_kernel, (int)(pl.units * pl.per_kv), pg::kJoinWarps * 32, 0, st, p) == cudaSuccess
+               ? KVPACK_OK : KVPACK_ERR_CUDA;
+}
+
+kvpack_status check_paged_pointers(const void *K, const void *V, const void *table, const void *lens) {
+    const void *ptrs[] = {K, V, table, lens};
+    for (const void *ptr : ptrs) {
+        if (ptr == nullptr) return KVPACK_ERR_INVALID_ARG;
+        if (!aligned16(ptr)) return KVPACK_ERR_ALIGNMENT;
+    }
+    return KVPACK_OK;
+}
+
+// A text tail in pages (decode_impl's K_text, V_text are then null)
+struct PagedText {
+    const kvpack_paged_dims *pd;
+    const uint16_t *K, *V;
+    const int32_t *table, *lens;
+};
+
 // 4-bit visual coefficients (quant.cuh) in place of the 16-bit planes
 struct Q4Planes {
     const uint8_t *QK_lo, *QK_hi, *QV_lo, *QV_hi;
     const int8_t *EK, *EV;
 };
 
-// The decode step; tb (the text tokens compressed with a basis of their own) and q4 (4-bit
-// visual coefficients, when CK_lo .. CV_hi are null) may be null.
+// The decode step; tb (the text tokens compressed with a basis of their own), q4 (4-bit visual
+// coefficients, when CK_lo .. CV_hi are null) and pt (the uncompressed tail in pages, when K_text
+// and V_text are null) may be null.
 kvpack_status decode_impl(const kvpack_dims *d, int32_t n_layers, const uint16_t *q, const uint16_t *CK_lo,
                           const uint16_t *CK_hi, const uint16_t *BK, const uint16_t *CV_lo, const uint16_t *CV_hi,
                           const uint16_t *BV, const Q4Planes *q4, const kvpack_text_basis *tb, const uint16_t *K_text,
                           const uint16_t *V_text, int32_t L_text, const uint32_t *mask, float softmax_scale,
-                          uint16_t *out, float *mass, void *ws, size_t ws_bytes, void *stream) {
+                          uint16_t *out, float *mass, void *ws, size_t ws_bytes, void *stream,
+                          const PagedText *pt = nullptr) {
     kvpack_status s = check_dims(d, n_layers);
     if (s != KVPACK_OK) return s;
+    if (pt != nullptr) {
+        if ((s = check_paged(pt->pd, n_layers)) != KVPACK_OK) return s;
+        if (pt->pd->batch != d->batch || pt->pd->n_q_heads != d->n_q_heads || pt->pd->n_kv_heads != d->n_kv_heads)
+            return KVPACK_ERR_INVALID_ARG;
+        if ((s = check_paged_pointers(pt->K, pt->V, pt->table, pt->lens)) != KVPACK_OK) return s;
+    }
     const int L_c = tb != nullptr ? tb->L_c : 0;
     if (tb != nullptr) {
         if (L_c < 0 || L_c > kMaxT) return KVPACK_ERR_INVALID_ARG;
@@ -420,10 +520,11 @@ kvpack_status decode_impl(const kvpack_dims *d, int32_t n_layers, const uint16_t
                           L_text > 0 ? K_text : nullptr, L_text > 0 ? V_text : nullptr};
     for (const void *ptr : ptrs)
         if (ptr && !aligned16(ptr)) return KVPACK_ERR_ALIGNMENT;
-    const DecodePlan pl = plan_decode(d, n_layers, L_c);
+    const DecodePlan pl = plan_decode(d, n_layers, L_c, pt != nullptr);
     if ((long long)pl.units * d->T_vis * 3 >= (1LL << 31)) return KVPACK_ERR_UNSUPPORTED;   // int32 rows
     if ((long long)pl.units * L_c * 3 >= (1LL << 31)) return KVPACK_ERR_UNSUPPORTED;
-    if (ws == nullptr || ws_bytes < pl.total) return KVPACK_ERR_WORKSPACE;
+    const size_t need = pl.total + (pt != nullptr ? plan_paged(pt->pd, n_layers).total : 0);
+    if (ws == nullptr || ws_bytes < need) return KVPACK_ERR_WORKSPACE;
     DeviceInfo *di = nullptr;
     if ((s = device_info(&di)) != KVPACK_OK) return s;
 
@@ -438,7 +539,8 @@ kvpack_status decode_impl(const kvpack_dims *d, int32_t n_layers, const uint16_t
     // on many units writes one partial per (unit, KV head)
     int ct = kTextChunk;
     while (ct < 1024 && (long long)pl.units * 4 * ((L_text + 2 * ct - 1) / (2 * ct)) >= 2LL * kPlanSMs * 8 * 2) ct <<= 1;
-    const int Sc = (L_text + ct - 1) / ct;
+    const int Sc_dense = (L_text + ct - 1) / ct;         // partials the text kernel writes
+    const int Sc = pt != nullptr ? 1 : Sc_dense;         // partials that are combined
     const float scale2 = softmax_scale * 1.4426950408889634f;
     unsigned char *w = static_cast<unsigned char *>(ws);
     unsigned char *qt = w + pl.off_qt;
@@ -452,6 +554,12 @@ kvpack_status decode_impl(const kvpack_dims *d, int32_t n_layers, const uint16_t
     float *vpart2 = L_c > 0 ? reinterpret_cast<float *>(w + pl.off_vp2) : nullptr;
     uint32_t *mask2 = L_c > 0 ? reinterpret_cast<uint32_t *>(w + pl.off_mask2) : nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+    // 0. a paged tail's softmax parts, joined to one partial per unit.  The text kernel is a plain
+    // launch: it starts after the join has ended, and so does all that reads the partials.
+    if (pt != nullptr && (s = launch_paged_attend(pt->pd, n_layers, q, pt->K, pt->V, pt->table, pt->lens, softmax_scale,
+                                                  nullptr, nullptr, tpart, w + pl.total, st)) != KVPACK_OK)
+        return s;
 
     // the text kernel's work counter starts at zero; the text tokens' own mask is all ones
     if (cudaMemsetAsync(counter, 0, 4 * sizeof(unsigned int), st) != cudaSuccess) return KVPACK_ERR_CUDA;
@@ -482,8 +590,8 @@ kvpack_status decode_impl(const kvpack_dims *d, int32_t n_layers, const uint16_t
         tp.q = q; tp.part = tpart; tp.qt = qt; tp.qt2 = qt2; tp.counter = counter;
         tp.qsplit = pl.NH == 28 ? 14 : 1 << 30;
         tp.n_units = pl.units; tp.L = L_text; tp.Hg = Hg; tp.per_kv = per_kv; tp.n_q = d->n_q_heads;
-        tp.groups = groups; tp.Sc = Sc; tp.ct = ct; tp.n_qitems = pl.units * 4 * (L_c > 0 ? 2 : 1);
-        tp.n_items = tp.n_qitems + pl.units * 4 * Sc; tp.scale2 = scale2;
+        tp.groups = groups; tp.Sc = Sc_dense; tp.ct = ct; tp.n_qitems = pl.units * 4 * (L_c > 0 ? 2 : 1);
+        tp.n_items = tp.n_qitems + pl.units * 4 * Sc_dense; tp.scale2 = scale2;
         const int grid = tp.n_items < di->sms ? tp.n_items : di->sms;
         dc::text::text_kernel<<<grid, dc::text::kThreads, dc::text::smem_bytes(), st>>>(tp);
         if (cudaGetLastError() != cudaSuccess) return KVPACK_ERR_CUDA;
@@ -918,6 +1026,173 @@ kvpack_status kvpack_compress(const kvpack_dims *d, int32_t n_layers, const uint
     }
     return kvpack::compress::run(units, d->T_vis, X, tm_x, C_lo, C_hi, B, sigma, ws, di->sms, max_iter,
                                  static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ positions and the paged cache
+
+namespace {
+
+namespace rp = kvpack::rope;
+
+kvpack_status check_spec(const kvpack_rope_spec *r) {
+    if (r->rotary_dim <= 0 || r->n_axes <= 0 || (r->adjacent != 0 && r->adjacent != 1)) return KVPACK_ERR_INVALID_ARG;
+    if (r->rotary_dim % 16 != 0 || r->rotary_dim > KVPACK_HEAD_DIM || r->n_axes > KVPACK_MAX_AXES)
+        return KVPACK_ERR_UNSUPPORTED;
+    for (int i = 0; i < r->rotary_dim / 2; ++i)
+        if (r->axis[i] >= r->n_axes) return KVPACK_ERR_INVALID_ARG;
+    return KVPACK_OK;
+}
+
+kvpack_status check_heads(const kvpack_heads *v) {
+    if (v == nullptr || v->data == nullptr) return KVPACK_ERR_INVALID_ARG;
+    if (!aligned16(v->data) || v->outer_stride % 8 != 0 || v->row_stride % 8 != 0 || v->group_stride % 8 != 0)
+        return KVPACK_ERR_ALIGNMENT;
+    return KVPACK_OK;
+}
+
+// An output is its input (rotation in place) only with the same strides.
+kvpack_status check_pair(const kvpack_heads *in, const kvpack_heads *out) {
+    kvpack_status s = check_heads(in);
+    if (s == KVPACK_OK) s = check_heads(out);
+    if (s != KVPACK_OK) return s;
+    if (in->data == out->data && (in->outer_stride != out->outer_stride || in->row_stride != out->row_stride ||
+                                  in->group_stride != out->group_stride))
+        return KVPACK_ERR_INVALID_ARG;
+    return KVPACK_OK;
+}
+
+inline rp::View view(const kvpack_heads *v) {
+    return rp::View{v->data, v->outer_stride, v->row_stride, v->group_stride};
+}
+
+void set_spec(rp::Params &p, const kvpack_rope_spec *r, const double *freq, const int32_t *pos, bool inverse) {
+    p.sign = inverse ? -1.f : 1.f;
+    if (r == nullptr) return;
+    p.freq = freq;
+    p.pos = pos;
+    p.rot8 = r->rotary_dim / 16;
+    for (int i = 0; i < r->rotary_dim / 2; ++i) p.axis2[i >> 4] |= (uint32_t)r->axis[i] << (2 * (i & 15));
+}
+
+// Splits of a row's heads over warps: one warp per row where the rows alone fill the GPU.
+template <bool APPEND>
+kvpack_status launch_rope(rp::Params &p, long long orows, bool adjacent, cudaStream_t st) {
+    const long long want = (long long)kPlanSMs * 32;
+    const long long splits = (want + orows - 1) / orows;
+    p.splits = (int)(splits < 1 ? 1 : splits > p.quads ? p.quads : splits);
+    p.qpw = (p.quads + p.splits - 1) / p.splits;
+    p.splits = (p.quads + p.qpw - 1) / p.qpw;
+    p.items = orows * p.splits;
+    const long long grid = (p.items + rp::kThreads / 32 - 1) / (rp::kThreads / 32);
+    if (grid > 0x7fffffffLL) return KVPACK_ERR_UNSUPPORTED;
+    if (adjacent) rp::rope_kernel<APPEND, true><<<(unsigned)grid, rp::kThreads, 0, st>>>(p);
+    else rp::rope_kernel<APPEND, false><<<(unsigned)grid, rp::kThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, const int32_t *pos, int32_t n_outer,
+                          int32_t n_rows, int32_t n_q, const kvpack_heads *q, const kvpack_heads *q_out, int32_t n_k,
+                          const kvpack_heads *k, const kvpack_heads *k_out, int32_t inverse, void *stream) {
+    if (spec == nullptr || n_outer <= 0 || n_rows < 0 || n_q < 0 || n_k < 0 || n_q + n_k <= 0)
+        return KVPACK_ERR_INVALID_ARG;
+    kvpack_status s = check_spec(spec);
+    if (s != KVPACK_OK) return s;
+    if (n_q > 1024 || n_k > 1024) return KVPACK_ERR_UNSUPPORTED;
+    if (n_rows == 0) return KVPACK_OK;
+    if (!freq || !pos) return KVPACK_ERR_INVALID_ARG;
+    if (!aligned16(freq) || !aligned16(pos)) return KVPACK_ERR_ALIGNMENT;
+    if (n_q > 0 && (s = check_pair(q, q_out)) != KVPACK_OK) return s;
+    if (n_k > 0 && (s = check_pair(k, k_out)) != KVPACK_OK) return s;
+    rp::Params p{};
+    if (n_q > 0) { p.q = view(q); p.q_out = view(q_out); }
+    if (n_k > 0) { p.k = view(k); p.k_out = view(k_out); }
+    set_spec(p, spec, freq, pos, inverse != 0);
+    p.rows = n_rows;
+    p.pos_outer = n_rows;
+    p.pos_axis = (long long)n_outer * n_rows;
+    p.n_q = n_q; p.n_k = n_k;
+    p.quads_q = (n_q + 3) / 4; p.quads_k = (n_k + 3) / 4; p.quads = p.quads_q + p.quads_k;
+    return launch_rope<false>(p, (long long)n_outer * n_rows, spec->adjacent != 0, static_cast<cudaStream_t>(stream));
+}
+
+kvpack_status kvpack_paged_append(const kvpack_paged_dims *d, int32_t n_layers, const kvpack_rope_spec *spec,
+                                  const double *freq, const int32_t *pos, int32_t n_rows, const kvpack_heads *q,
+                                  const kvpack_heads *k, const kvpack_heads *v, const int32_t *row_offsets,
+                                  const int32_t *seq_lens, const int32_t *block_table, const kvpack_heads *q_out,
+                                  uint16_t *K_pages, uint16_t *V_pages, void *stream) {
+    kvpack_status s = check_paged(d, n_layers);
+    if (s != KVPACK_OK) return s;
+    if (n_rows < 0 || (row_offsets == nullptr && n_rows != d->batch)) return KVPACK_ERR_INVALID_ARG;
+    if (spec != nullptr && (s = check_spec(spec)) != KVPACK_OK) return s;
+    if (n_rows == 0) return KVPACK_OK;
+    if (spec != nullptr && (!freq || !pos)) return KVPACK_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr)) return KVPACK_ERR_INVALID_ARG;
+    if ((s = check_heads(k)) != KVPACK_OK || (s = check_heads(v)) != KVPACK_OK) return s;
+    if (q != nullptr && (s = check_pair(q, q_out)) != KVPACK_OK) return s;
+    if ((s = check_paged_pointers(K_pages, V_pages, block_table, seq_lens)) != KVPACK_OK) return s;
+    const void *ptrs[] = {freq, pos, row_offsets};
+    for (const void *ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return KVPACK_ERR_ALIGNMENT;
+    rp::Params p{};
+    if (q != nullptr) { p.q = view(q); p.q_out = view(q_out); }
+    p.k = view(k);
+    p.v = view(v);
+    set_spec(p, spec, freq, pos, false);
+    p.rows = n_rows;
+    p.pos_axis = n_rows;
+    p.pos_outer = 0;
+    p.n_q = q != nullptr ? d->n_q_heads : 0;
+    p.n_k = d->n_kv_heads;
+    p.quads_q = (p.n_q + 3) / 4; p.quads_k = (p.n_k + 3) / 4; p.quads = p.quads_q + 2 * p.quads_k;
+    p.K = K_pages; p.V = V_pages; p.table = block_table; p.lens = seq_lens; p.offsets = row_offsets;
+    p.batch = d->batch; p.n_pages = d->n_pages; p.max_pages = d->max_pages; p.page_shift = log2_exact(d->page_size);
+    return launch_rope<true>(p, (long long)n_layers * n_rows, spec != nullptr && spec->adjacent != 0,
+                             static_cast<cudaStream_t>(stream));
+}
+
+size_t kvpack_paged_decode_workspace(const kvpack_paged_dims *d, int32_t n_layers) {
+    if (check_paged(d, n_layers) != KVPACK_OK) return 0;
+    return plan_paged(d, n_layers).total;
+}
+
+kvpack_status kvpack_paged_decode_attn(const kvpack_paged_dims *d, int32_t n_layers, const uint16_t *q,
+                                       const uint16_t *K_pages, const uint16_t *V_pages, const int32_t *block_table,
+                                       const int32_t *seq_lens, float softmax_scale, uint16_t *out, float *lse, void *ws,
+                                       size_t ws_bytes, void *stream) {
+    kvpack_status s = check_paged(d, n_layers);
+    if (s != KVPACK_OK) return s;
+    if (!q || !out) return KVPACK_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || softmax_scale > 3.402823466e38f) return KVPACK_ERR_INVALID_ARG;
+    if ((s = check_paged_pointers(K_pages, V_pages, block_table, seq_lens)) != KVPACK_OK) return s;
+    const void *ptrs[] = {q, out, lse, ws};
+    for (const void *ptr : ptrs)
+        if (ptr && !aligned16(ptr)) return KVPACK_ERR_ALIGNMENT;
+    if (ws == nullptr || ws_bytes < plan_paged(d, n_layers).total) return KVPACK_ERR_WORKSPACE;
+    return launch_paged_attend(d, n_layers, q, K_pages, V_pages, block_table, seq_lens, softmax_scale, out, lse, nullptr,
+                               ws, static_cast<cudaStream_t>(stream));
+}
+
+size_t kvpack_decode_paged_workspace(const kvpack_dims *d, const kvpack_paged_dims *pd, int32_t n_layers) {
+    if (check_dims(d, n_layers) != KVPACK_OK || check_paged(pd, n_layers) != KVPACK_OK) return 0;
+    return plan_decode(d, n_layers, 0, true).total + plan_paged(pd, n_layers).total;
+}
+
+kvpack_status kvpack_decode_attn_paged(const kvpack_dims *d, const kvpack_paged_dims *pd, int32_t n_layers,
+                                       const uint16_t *q, const uint16_t *CK_lo, const uint16_t *CK_hi,
+                                       const uint16_t *BK, const uint16_t *CV_lo, const uint16_t *CV_hi,
+                                       const uint16_t *BV, const uint16_t *K_pages, const uint16_t *V_pages,
+                                       const int32_t *block_table, const int32_t *seq_lens, const uint32_t *mask,
+                                       float softmax_scale, uint16_t *out, float *mass, void *ws, size_t ws_bytes,
+                                       void *stream) {
+    const PagedText pt{pd, K_pages, V_pages, block_table, seq_lens};
+    return decode_impl(d, n_layers, q, CK_lo, CK_hi, BK, CV_lo, CV_hi, BV, nullptr, nullptr, nullptr, nullptr, 0, mask,
+                       softmax_scale, out, mass, ws, ws_bytes, stream, &pt);
 }
 
 }  // extern "C"
