@@ -31,15 +31,11 @@ torch.int32 holding the uint32 words; fp32 arrays are torch.float32.
 from ._lib import (  # noqa: F401
     Dims,
     KvpackError,
-    PagedDims,
-    Rope,
     STATUS_NAMES,
     compress,
     compress_workspace,
     decode_attn,
     decode_attn_noalloc,
-    decode_attn_paged,
-    decode_paged_workspace,
     decode_attn_tb,
     decode_tb_workspace,
     decode_attn_q4,
@@ -53,11 +49,17 @@ from ._lib import (  # noqa: F401
     last_device_status,
     lib,
     library_path,
+    select,
+    selftest_bounded_wait,
+    version,
+)
+from ._paged import (  # noqa: F401
+    PagedDims,
+    Rope,
+    decode_attn_paged,
+    decode_paged_workspace,
     paged_append,
     paged_decode_attn,
     paged_decode_workspace,
     rope,
-    select,
-    selftest_bounded_wait,
-    version,
 )

@@ -1,12 +1,16 @@
-"""Build libkvpack.so (the sm_100a kernels and their C ABI) in-tree with nvcc."""
+"""Build in-tree: libkvpack.so (the sm_100a kernels and their C ABI) with nvcc, and _call.so (the native part of
+the Python binding) with the C++ compiler against torch's headers."""
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvpack.so")
+CALL = os.path.join(HERE, "_call.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -35,5 +39,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build_call(force: bool = False) -> str:
+    """The binding's extension; it links to libkvpack.so next to it."""
+    src = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "kvpack.h")]
+    if not force and os.path.exists(CALL) and os.path.getmtime(CALL) >= max(os.path.getmtime(s) for s in src):
+        return CALL
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-w", *(f"-I{i}" for i in inc),
+           "-o", CALL + ".tmp", src[0], f"-L{HERE}", "-l:libkvpack.so", f"-L{os.path.join(torch, 'lib')}", "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.check_call(cmd)
+    os.replace(CALL + ".tmp", CALL)
+    return CALL
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_call(force="--force" in sys.argv))

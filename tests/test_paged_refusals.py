@@ -21,18 +21,22 @@ def _pd(kv, **over):
     return kv.PagedDims(**{**base, **over})
 
 
+class _CHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("outer", ctypes.c_int64), ("row", ctypes.c_int64), ("group", ctypes.c_int64)]
+
+
 def _heads(kv, data=P, strides=(0, 4096, 512)):
-    return kv._lib._CHeads(data, *strides)
+    return ctypes.pointer(_CHeads(data, *strides))
 
 
 def _rope(kv, spec=None, rows=4, n_q=2, n_k=0, outer=1, freq=P, pos=P, q=None, q_out=None, raw=None):
-    c = (spec or kv.Rope())._c if raw is None else raw
+    c = ctypes.byref((spec or kv.Rope())._c if raw is None else raw)
     q = q or _heads(kv)
-    return kv.lib().kvpack_rope(c, freq, pos, outer, rows, n_q, q, q_out or _heads(kv, 2 * P), n_k, None, None, 0, None)
+    return _L(kv).kvpack_rope(c, freq, pos, outer, rows, n_q, q, q_out or _heads(kv, 2 * P), n_k, None, None, 0, None)
 
 
 def test_rope_refusals(kv):
-    R = kv._lib._CRopeSpec
+    R = kv._paged._CRopeSpec
     none = (ctypes.c_uint8 * 64)()
     assert _rope(kv, raw=R(0, 1, 0, none)) == 1
     assert _rope(kv, raw=R(128, 0, 0, none)) == 1
@@ -63,9 +67,18 @@ def test_rope_spec_refusals(kv):
     assert kv.Rope(n_axes=3, sections=(16, 24, 24)).axis_of_pair == (0,) * 16 + (1,) * 24 + (2,) * 24
 
 
+def _L(kv):
+    """The C entry points with untyped pointers."""
+    L, vp, i32 = ctypes.CDLL(kv.library_path()), ctypes.c_void_p, ctypes.c_int32
+    L.kvpack_rope.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, i32, vp]
+    L.kvpack_paged_append.argtypes = [vp, i32, vp, vp, vp, i32, *([vp] * 10)]
+    L.kvpack_paged_decode_attn.argtypes = [vp, i32, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
+    return L
+
+
 def _attend(kv, d, n_layers=1, q=P, table=P, lens=P, scale=1.0, out=P, lse=P, ws=P, ws_bytes=None):
     n = kv.paged_decode_workspace(d, n_layers) if ws_bytes is None else ws_bytes
-    return kv.lib().kvpack_paged_decode_attn(d.c(), n_layers, q, P, P, table, lens, scale, out, lse, ws, n, None)
+    return _L(kv).kvpack_paged_decode_attn(d._at, n_layers, q, P, P, table, lens, scale, out, lse, ws, n, None)
 
 
 @pytest.mark.parametrize("over,status", [
@@ -78,7 +91,7 @@ def test_paged_shape_refusals(kv, over, status):
     assert kv.paged_decode_workspace(d, 1) == 0
     assert _attend(kv, d, ws_bytes=1 << 40) == status
     h = _heads(kv)
-    assert kv.lib().kvpack_paged_append(d.c(), 1, None, None, None, d.batch, None, h, h, None, P, P, None, P, P, None) == status
+    assert _L(kv).kvpack_paged_append(d._at, 1, None, None, None, d.batch, None, h, h, None, P, P, None, P, P, None) == status
 
 
 def test_paged_decode_refusals(kv):
@@ -99,7 +112,7 @@ def test_paged_append_refusals(kv):
     d, h = _pd(kv), _heads(kv)
 
     def call(spec=None, freq=None, pos=None, rows=3, q=None, k=h, v=h, off=None, lens=P, table=P, q_out=None, K=P, L=1):
-        return kv.lib().kvpack_paged_append(d.c(), L, spec, freq, pos, rows, q, k, v, off, lens, table, q_out, K, P, None)
+        return _L(kv).kvpack_paged_append(d._at, L, spec, freq, pos, rows, q, k, v, off, lens, table, q_out, K, P, None)
 
     assert call(L=0) == 1
     assert call(rows=4) == 1                       # one row per sequence without offsets
@@ -108,8 +121,8 @@ def test_paged_append_refusals(kv):
     assert call(v=_heads(kv, P, (0, 4, 512))) == 2
     assert call(q=h) == 1                          # q without q_out
     assert call(q=h, q_out=_heads(kv, P, (0, 8192, 512))) == 1
-    assert call(spec=kv.Rope()._c, pos=P) == 1     # no frequencies
-    assert call(spec=kv.Rope()._c, freq=P, pos=P + 8) == 2
+    assert call(spec=kv.Rope()._at, pos=P) == 1     # no frequencies
+    assert call(spec=kv.Rope()._at, freq=P, pos=P + 8) == 2
     assert call(off=P + 4) == 2
     assert call(lens=None) == 1
     assert call(K=P + 8) == 2
@@ -123,7 +136,7 @@ def test_decode_attn_paged_refusals(kv):
     assert n > kv.decode_workspace(d, 2)
 
     def call(dd=d, pp=pd, table=P, ws_bytes=n, scale=1.0):
-        return kv.lib().kvpack_decode_attn_paged(ctypes.byref(dd.c()), pp.c(), 2, *([P] * 9), table, P, P, scale, P, P, P,
+        return kv.lib().kvpack_decode_attn_paged(ctypes.byref(dd.c()), pp._at, 2, *([P] * 9), table, P, P, scale, P, P, P,
                                                  ws_bytes, None)
 
     assert call(pp=_pd(kv, batch=4)) == 1
@@ -136,51 +149,84 @@ def test_decode_attn_paged_refusals(kv):
     assert kv.decode_paged_workspace(d, _pd(kv, page_size=8), 2) == 0
 
 
-def test_the_binding_refuses_tensors_that_are_not_on_the_current_device(kv, monkeypatch):
-    monkeypatch.setattr(kv._lib, "_device", lambda: 0)
+# The binding compares devices last: tensors on the CPU that pass every other check are refused there, so that all of
+# them can be seen without a GPU.
+
+def _ok(kv):
+    """Arguments that only their device speaks against."""
     d, spec = _pd(kv), kv.Rope()
-    x = torch.zeros(3, 16, 128, dtype=torch.bfloat16)
-    lens, table = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 5, dtype=torch.int32)
-    pool = torch.zeros(1, 10, 8, 64, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="device"):
-        kv.rope(spec, spec.frequencies(device="cpu"), torch.zeros(1, 3, dtype=torch.int32), x, x)
-    with pytest.raises(ValueError, match="device"):
-        kv.paged_append(d, 1, None, None, None, None, x[:, :8], x[:, 8:], None, lens, table, None, pool, pool)
-    with pytest.raises(ValueError, match="device"):
-        kv.paged_decode_attn(d, 1, x, pool, pool, table, lens, 1.0, x, None, pool)
+    x = torch.zeros(3, 32, 128, dtype=torch.bfloat16)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    rope = dict(spec=spec, freq=spec.frequencies(device="cpu"), pos=torch.zeros(1, 3, dtype=torch.int32), q=x[:, :16],
+                q_out=z(3, 16, 128), k=x[:, 16:24], k_out=z(3, 8, 128))
+    pool = dict(K_pages=z(1, 10, 8, 64, 128), V_pages=z(1, 10, 8, 64, 128), block_table=torch.zeros(3, 5, dtype=torch.int32),
+                seq_lens=torch.zeros(3, dtype=torch.int32))
+    append = dict(dims=d, n_layers=1, **rope, v=x[:, 24:], row_offsets=None, **pool)
+    del append["k_out"]
+    attend = dict(dims=d, n_layers=1, q=z(3, 16, 128), **pool, scale=1.0, out=z(3, 16, 128), lse=torch.zeros(3, 16),
+                  ws=torch.zeros(100, dtype=torch.uint8))
+    return {"rope": rope, "paged_append": append, "paged_decode_attn": attend}
 
 
-class _Fake:
-    """A tensor's outside, as the binding's checks see it."""
+BF = torch.bfloat16
+BAD = [
+    ("rope", dict(spec=3), TypeError, "Rope"),
+    ("rope", dict(q=None), ValueError, "an input and its output"),
+    ("rope", dict(q=None, q_out=None, k=None, k_out=None), ValueError, "an input and its output"),
+    ("rope", dict(q=7), TypeError, "q is not a tensor"),
+    ("rope", dict(pos=torch.zeros(1, 3)), ValueError, "pos is Float"),
+    ("rope", dict(pos=torch.zeros(2, 3, dtype=torch.int32)), ValueError, "pos has shape"),
+    ("rope", dict(pos=torch.zeros(3, dtype=torch.int32)), ValueError, "pos has shape"),
+    ("rope", dict(pos=torch.zeros(3, 1, dtype=torch.int32).expand(3, 3)[:1, :].T.contiguous()), ValueError, "pos has shape"),
+    ("rope", dict(freq=torch.zeros(64)), ValueError, "freq is Float"),
+    ("rope", dict(freq=torch.zeros(32, dtype=torch.float64)), ValueError, "freq has shape"),
+    ("rope", dict(q=torch.zeros(4, 16, 128, dtype=BF)), ValueError, "q has shape"),
+    ("rope", dict(q_out=torch.zeros(3, 8, 128, dtype=BF)), ValueError, "q_out has shape"),
+    ("rope", dict(q=torch.zeros(3, 16, 64, dtype=BF)), ValueError, "q has shape"),
+    ("rope", dict(q=torch.zeros(16, 128, dtype=BF)), ValueError, "q has shape"),
+    ("rope", dict(q=torch.zeros(3, 16, 128, dtype=torch.float16)), ValueError, "q is Half"),
+    ("rope", dict(q=torch.zeros(3, 32, 128, dtype=BF)[:, ::2]), ValueError, "side by side"),
+    ("rope", dict(k=torch.zeros(3, 8, 256, dtype=BF)[..., ::2]), ValueError, "side by side"),
+    ("rope", dict(nothing=1), TypeError, "unexpected"),
+    ("paged_append", dict(dims=None), TypeError, "PagedDims"),
+    ("paged_append", dict(n_layers=2), ValueError, "k has shape"),
+    ("paged_append", dict(n_layers=2 ** 40), ValueError, "n_layers"),
+    ("paged_append", dict(k=torch.zeros(4, 8, 128, dtype=BF)), ValueError, "one row per sequence"),
+    ("paged_append", dict(v=torch.zeros(3, 7, 128, dtype=BF)), ValueError, "v has shape"),
+    ("paged_append", dict(q_out=None), ValueError, "q and q_out"),
+    ("paged_append", dict(row_offsets=torch.zeros(3, dtype=torch.int32)), ValueError, "row_offsets has shape"),
+    ("paged_append", dict(seq_lens=torch.zeros(3, dtype=torch.int64)), ValueError, "seq_lens is Long"),
+    ("paged_append", dict(K_pages=torch.zeros(1, 9, 8, 64, 128, dtype=BF)), ValueError, "K_pages has shape"),
+    ("paged_append", dict(pos=torch.zeros(3, 3, dtype=torch.int32)), ValueError, "pos has shape"),
+    ("paged_decode_attn", dict(q=torch.zeros(3, 8, 128, dtype=BF)), ValueError, "q has shape"),
+    ("paged_decode_attn", dict(q=torch.zeros(3, 32, 128, dtype=BF)[:, :16]), ValueError, "contiguous"),
+    ("paged_decode_attn", dict(lse=torch.zeros(3, 16, dtype=BF)), ValueError, "lse is BFloat16"),
+    ("paged_decode_attn", dict(block_table=torch.zeros(5, 3, dtype=torch.int32).T), ValueError, "contiguous"),
+    ("paged_decode_attn", dict(block_table=torch.zeros(3, 6, dtype=torch.int32)), ValueError, "block_table has shape"),
+    ("paged_decode_attn", dict(V_pages=torch.zeros(1, 10, 8, 64, 128)), ValueError, "V_pages is Float"),
+    ("paged_decode_attn", dict(ws=torch.zeros(100)), ValueError, "ws is Float"),
+    ("paged_decode_attn", dict(scale="x"), TypeError, "real number"),
+]
 
-    def __init__(self, *shape, dtype="torch.bfloat16", device=0, stride=None):
-        t = torch.empty(shape, device="meta")
-        self.shape, self.dtype, self._d, self._s = t.shape, dtype, device, stride or t.stride()
-        self._c = stride is None
 
-    def get_device(self): return self._d
-    def stride(self): return self._s
-    def dim(self): return len(self.shape)
-    def numel(self): return self.shape.numel()
-    def is_contiguous(self): return self._c
-    def data_ptr(self): return P
+@pytest.mark.parametrize("call", ["rope", "paged_append", "paged_decode_attn"])
+def test_the_binding_refuses_tensors_that_are_not_on_the_current_device(kv, call):
+    with pytest.raises(ValueError, match="is not on the current CUDA device"):
+        getattr(kv, call)(**_ok(kv)[call])
 
 
-def test_the_binding_refuses_shapes_types_and_strides(kv):
-    L = kv._lib
-    with pytest.raises(ValueError, match="shape"):
-        L._want(_Fake(3, 4), 0, "x", ("torch.bfloat16",), shape=(3, 5))
-    with pytest.raises(ValueError, match="is torch.float32"):
-        L._want(_Fake(3, 4, dtype="torch.float32"), 0, "x", ("torch.bfloat16",), shape=(3, 4))
-    with pytest.raises(ValueError, match="contiguous"):
-        L._want(_Fake(3, 4, stride=(8, 1)), 0, "x", ("torch.bfloat16",), shape=(3, 4))
-    with pytest.raises(ValueError, match="device"):
-        L._want(_Fake(3, 4, device=1), 0, "x", ("torch.bfloat16",), shape=(3, 4))
-    ok = L._heads(_Fake(7, 6, 128), 0, "x", 1, 7, 6)
-    assert (ok.row_stride, ok.group_stride) == (768, 512)
-    ok = L._heads(_Fake(2, 3, 7, 4, 128), 0, "x", 2, 7, 12)
-    assert (ok.outer_stride, ok.row_stride, ok.group_stride) == (3 * 7 * 512, 512, 7 * 512)
-    for bad in (_Fake(7, 6, 64), _Fake(8, 6, 128), _Fake(2, 7, 6, 128), _Fake(7, 6, 128, stride=(768, 256, 1)),
-                _Fake(7, 6, 128, stride=(1536, 128, 2)), _Fake(1, 2, 7, 3, 128)):
-        with pytest.raises(ValueError):
-            L._heads(bad, 0, "x", 1, 7, 6)
+@pytest.mark.parametrize("call,over,error,text", BAD)
+def test_the_binding_refuses(kv, call, over, error, text):
+    args = {**_ok(kv)[call], **over}
+    with pytest.raises(error, match=text):
+        getattr(kv, call)(**args)
+
+
+def test_the_binding_takes_arguments_once(kv):
+    a = _ok(kv)["rope"]
+    with pytest.raises(TypeError, match="twice"):
+        kv.rope(a["spec"], spec=a["spec"])
+    with pytest.raises(TypeError, match="needs"):
+        kv.rope(a["spec"])
+    with pytest.raises(TypeError, match="at most"):
+        kv.rope(*range(10))
