@@ -159,6 +159,13 @@ bool rs_attrs() {
            rs_attr<32, false, true>() && rs_attr<32, true, true>();
 }
 
+bool paged_attrs() {
+    namespace pg = kvpack::paged;
+    return cudaFuncSetAttribute(pg::attend_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
+           cudaFuncSetAttribute(pg::unit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                pg::kWarps * pg::kRingBytes) == cudaSuccess;
+}
+
 // Launch on `st` with programmatic stream serialization: the kernel may start while the
 // previous kernel on the stream drains, and waits for it (griddep_wait) before reading its
 // outputs.
@@ -271,7 +278,7 @@ kvpack_status device_info(DeviceInfo **out) {
                                  (int)dc::text::smem_bytes()) != cudaSuccess ||
             cudaFuncSetAttribute(dc::text::text_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
                 cudaSuccess ||
-            !rs_attrs() ||
+            !rs_attrs() || !paged_attrs() ||
             cudaFuncSetAttribute(kvpack::baseline::decompress_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)sizeof(kvpack::baseline::DecSmem)) != cudaSuccess)
             return KVPACK_ERR_CUDA;
@@ -397,6 +404,8 @@ kvpack_status check_paged(const kvpack_paged_dims *d, int32_t n_layers) {
         return KVPACK_ERR_UNSUPPORTED;
     if ((long long)d->max_pages * d->page_size > KVPACK_MAX_PAGED_TOKENS) return KVPACK_ERR_UNSUPPORTED;
     if ((long long)n_layers * d->batch * d->n_q_heads > (1LL << 30)) return KVPACK_ERR_UNSUPPORTED;
+    const long long units = (long long)n_layers * d->batch * d->n_kv_heads;
+    if (units * ((long long)d->max_pages * d->page_size / 16) > (1LL << 40)) return KVPACK_ERR_UNSUPPORTED;   // tiles
     return KVPACK_OK;
 }
 
@@ -408,28 +417,55 @@ inline int log2_exact(int x) {
 
 struct PagedPlan {
     long long units;
-    int per_kv, grid;
-    size_t off_stat, off_acc, off_desc, total;
+    int per_kv, slots, grid, cluster;   // cluster: blocks per unit, 0 where the runs cross units
+    size_t off_stat, off_acc, total;
 };
 
-// One wave of a full B200, fewer blocks where the tables' capacity cannot give every warp a run.
+// A cluster per unit where the tables' capacity gives a warp at most this many tiles: with more, one
+// long sequence in a batch of short ones would keep its cluster busy alone.  Both forms measured, bf16,
+// 32 query and 8 cached heads, us (unit, runs): 1 x 1024 tokens 5.3 6.9, 16 x 1024 12.6 16.5, 32 x 1024
+// 28.7 30.7, 64 x 512 28.3 31.1; longest of a ragged batch: 16 x 2048 17.7 17.9, 32 x 4096 51.5 53.3.
+constexpr int kUnitTiles = 16;
+
+// Runs for a full B200, fewer where the tables' capacity cannot fill them.
 PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     PagedPlan pl{};
     pl.units = (long long)n_layers * d->batch * d->n_kv_heads;
     pl.per_kv = d->n_q_heads / d->n_kv_heads;
-    const long long tiles = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile);
-    const long long blocks = (tiles + pg::kMinTiles - 1) / pg::kMinTiles;   // runs; one per block, at first
-    pl.grid = (int)(blocks < kPlanSMs * pg::kBlocksPerSM ? blocks : kPlanSMs * pg::kBlocksPerSM);
-    const size_t slots = 2 * (size_t)pl.grid * pg::kWarps;
+    const long long places = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile + 1);
+    const long long runs = (places + pg::kMinPlaces - 1) / pg::kMinPlaces;
+    pl.slots = (int)(runs < kPlanSMs * pg::kSlotsPerSM ? runs : kPlanSMs * pg::kSlotsPerSM);
+    pl.grid = pl.slots * (1 + pg::kSecond);
+    const long long wave = kPlanSMs * pg::kUnitBlocksPerSM, cap = (long long)d->max_pages * d->page_size / pg::kTile;
+    int S = pl.units * 8 <= wave ? 8 : pl.units * 4 <= wave ? 4 : pl.units <= wave ? 2 : 1;
+    while (S > 1 && cap * 2 <= (long long)S * pg::kWarps) S >>= 1;       // two warps a tile are too many
+    // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 33.7, 28.9)
+    if (pl.units <= 2 * wave && cap <= (long long)S * pg::kWarps * kUnitTiles) pl.cluster = S;
+    const size_t slots = pl.cluster > 0 ? 0 : 2 * (size_t)pl.grid;
     size_t off = 0;
     pl.off_stat = off;
     off = align256(off + slots * 8 * 2 * sizeof(float));
     pl.off_acc = off;
     off = align256(off + slots * pl.per_kv * 128 * sizeof(float));
-    pl.off_desc = off;
-    off = align256(off + (size_t)pl.units * sizeof(int2));
-    pl.total = off;
+    pl.total = off > 0 ? off : 256;
     return pl;
+}
+
+cudaError_t launch_unit(const pg::Params &p, const PagedPlan &pl, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(pl.units * pl.cluster));
+    cfg.blockDim = dim3(pg::kThreads);
+    cfg.dynamicSmemBytes = pg::kWarps * pg::kRingBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)pl.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pg::unit_kernel, p, pl.cluster);
 }
 
 // out and lse of every unit, or (out null) the softmax parts of every query head in the text tail's
@@ -443,15 +479,25 @@ kvpack_status launch_paged_attend(const kvpack_paged_dims *d, int32_t n_layers, 
     p.q = q; p.K = K; p.V = V; p.table = table; p.lens = lens; p.out = out; p.lse = lse; p.tpart = tpart;
     p.stat = reinterpret_cast<float *>(w + pl.off_stat);
     p.acc = reinterpret_cast<float *>(w + pl.off_acc);
-    p.desc = reinterpret_cast<int2 *>(w + pl.off_desc);
     p.layers = n_layers; p.batch = d->batch; p.n_kv = d->n_kv_heads; p.per_kv = pl.per_kv;
     p.n_pages = d->n_pages; p.max_pages = d->max_pages; p.page_shift = log2_exact(d->page_size);
-    p.warps = pl.grid * pg::kWarps;
+    p.slots = pl.slots;
     p.scale2 = softmax_scale * 1.4426950408889634f;
-    pg::attend_kernel<<<pl.grid, pg::kThreads, (d->batch + 1) * sizeof(long long), st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return KVPACK_ERR_CUDA;
-    return launch_pdl(pg::join_kernel, (int)(pl.units * pl.per_kv), pg::kJoinWarps * 32, 0, st, p) == cudaSuccess
-               ? KVPACK_OK : KVPACK_ERR_CUDA;
+    if (pl.cluster > 0) return launch_unit(p, pl, st) == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
+    if (launch_pdl(pg::attend_kernel, pl.grid, 32, pg::kRingBytes, st, p) != cudaSuccess)
+        return KVPACK_ERR_CUDA;
+    const long long rows = pl.units * pl.per_kv;
+    // warps per row: so many that each has about four parts
+    const long long parts = pl.slots / pl.units + 1;
+    cudaError_t e;
+    if (parts > 16) e = launch_pdl(pg::join_kernel<8>, (int)rows, 256, 0, st, p, rows);
+    else if (parts > 8) e = launch_pdl(pg::join_kernel<4>, (int)((rows + 1) / 2), 256, 0, st, p, rows);
+    else if (parts > 4) e = launch_pdl(pg::join_kernel<2>, (int)((rows + 3) / 4), 256, 0, st, p, rows);
+    else {
+        const long long blocks = (rows + 7) / 8, most = kPlanSMs * 4;
+        e = launch_pdl(pg::join_kernel<1>, (int)(blocks < most ? blocks : most), 256, 0, st, p, rows);
+    }
+    return e == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
 }
 
 kvpack_status check_paged_pointers(const void *K, const void *V, const void *table, const void *lens) {
@@ -1087,9 +1133,9 @@ kvpack_status launch_rope(rp::Params &p, long long orows, bool adjacent, cudaStr
     p.items = orows * p.splits;
     const long long grid = (p.items + rp::kThreads / 32 - 1) / (rp::kThreads / 32);
     if (grid > 0x7fffffffLL) return KVPACK_ERR_UNSUPPORTED;
-    if (adjacent) rp::rope_kernel<APPEND, true><<<(unsigned)grid, rp::kThreads, 0, st>>>(p);
-    else rp::rope_kernel<APPEND, false><<<(unsigned)grid, rp::kThreads, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
+    const cudaError_t e = adjacent ? launch_pdl(rp::rope_kernel<APPEND, true>, (int)grid, rp::kThreads, 0, st, p)
+                                   : launch_pdl(rp::rope_kernel<APPEND, false>, (int)grid, rp::kThreads, 0, st, p);
+    return e == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
 }
 
 }  // namespace
@@ -1174,6 +1220,8 @@ kvpack_status kvpack_paged_decode_attn(const kvpack_paged_dims *d, int32_t n_lay
     for (const void *ptr : ptrs)
         if (ptr && !aligned16(ptr)) return KVPACK_ERR_ALIGNMENT;
     if (ws == nullptr || ws_bytes < plan_paged(d, n_layers).total) return KVPACK_ERR_WORKSPACE;
+    DeviceInfo *di = nullptr;                            // kernel attributes of the device
+    if ((s = device_info(&di)) != KVPACK_OK) return s;
     return launch_paged_attend(d, n_layers, q, K_pages, V_pages, block_table, seq_lens, softmax_scale, out, lse, nullptr,
                                ws, static_cast<cudaStream_t>(stream));
 }

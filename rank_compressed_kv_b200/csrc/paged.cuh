@@ -18,11 +18,14 @@ namespace kvpack {
 namespace paged {
 
 constexpr int kTile = 16;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;           // of unit_kernel's blocks
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSM = 3;
-constexpr int kMinTiles = 2;        // shortest run of a warp
-constexpr int kMaxBatch = 4096;
+constexpr int kSlotsPerSM = 8;      // runs of the first share per SM
+constexpr int kTwoShares = 64, kCut = 12, kSecond = 1;
+constexpr int kUnitBlocksPerSM = 2; // of unit_kernel
+constexpr int kSlots = 3;           // tiles of a warp in shared memory
+constexpr int kMinPlaces = 2;       // shortest run
+constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct Params {
@@ -31,18 +34,17 @@ struct Params {
     uint16_t *out;                  // [layers * batch][n_q][128], or null: tpart
     float *lse;                     // [layers * batch][n_q] or null
     float *tpart;                   // [layers * batch][n_q][kTxtPart]: (m, l, sum p V) of each head, or null
-    float *stat;                    // [2 * warps][8][2]: m, l of a run's part; slot 2 w for the unit that an
-    float *acc;                     // [2 * warps][per_kv][128]     earlier warp began, 2 w + 1 for the one it leaves
-    int2 *desc;                     // [units]: first warp and number of parts
-    int layers, batch, n_kv, per_kv, n_pages, max_pages, page_shift, warps;
+    float *stat;                    // [2 * runs][8][2]: m, l of a run's part; slot 2 w for the unit that an
+    float *acc;                     // [2 * runs][per_kv][128]     earlier run began, 2 w + 1 for the one it leaves
+    int layers, batch, n_kv, per_kv, n_pages, max_pages, page_shift, slots;   // slots: runs of the first share, at most
     float scale2;
 };
 
 struct Cursor {
     int b, lk, t, nt, len;          // sequence, layer * n_kv + KV head, tile, tiles and length of the sequence
+    long long x;                    // place among all (attend_kernel)
 };
 
-// Tiles of every sequence, summed up: pre[b] tiles (of one layer and KV head) before sequence b.
 __device__ __forceinline__ int clamped_len(const Params &p, int b, bool report) {
     const long long cap = (long long)p.max_pages << p.page_shift;
     int len = __ldg(p.lens + b);
@@ -53,180 +55,153 @@ __device__ __forceinline__ int clamped_len(const Params &p, int b, bool report) 
     return len;
 }
 
-__device__ __forceinline__ void scan_tiles(const Params &p, long long *pre) {
-    __shared__ long long wsum[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long carry = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long v = b < p.batch ? (clamped_len(p, b, blockIdx.x == 0) + kTile - 1) / kTile : 0;
+__device__ __forceinline__ void copy16(uint32_t dst, const uint16_t *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// The softmax state of a run's current unit, as the matrix instructions lay it out.  Lane 4 g + t:
+// m, l of heads 2t, 2t + 1; o[c / 2][2 (c % 2) + e]: entry 8 c + g of head 2t + e (c < 16).
+struct State {
+    float m[2], l[2], o[8][4];
+
+    __device__ __forceinline__ void clear() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
         #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += o;
-        }
-        if (lane == 31) wsum[warp] = v;
-        __syncthreads();
-        long long before = carry;
-        for (int w = 0; w < warp; ++w) before += wsum[w];
-        if (b < p.batch) pre[b + 1] = before + v;
-        for (int w = 0; w < kWarps; ++w) carry += wsum[w];
-        __syncthreads();
+        for (int e = 0; e < 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
     }
-    if (tid == 0) pre[0] = 0;
-    __syncthreads();
-}
+    // every lane's share of the sums
+    __device__ __forceinline__ void sum_lanes() {
+        #pragma unroll
+        for (int e = 0; e < 2; ++e)
+            #pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+    }
+    // head 2t + e unnormalised: dst[0 .. 127]
+    __device__ __forceinline__ void store(int e, int g, float *dst) const {
+        #pragma unroll
+        for (int c = 0; c < 16; ++c) dst[8 * c + g] = o[c >> 1][2 * (c & 1) + e];
+    }
+};
 
-__device__ __forceinline__ uint4 ldg_stream(const uint16_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
+// A warp's ring of tiles in shared memory: 16 rows of K, then 16 of V, 256 bytes each, 16-byte chunk
+// c of row r at c ^ (r & 7), so that eight rows of one chunk lie in different banks.
+constexpr int kTileBytes = 2 * kTile * 256;
+constexpr int kRingBytes = kSlots * kTileBytes;          // of a warp
 
-__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// No shared memory holds keys or values: the order of the 128 entries of q . K is free as long as
-// q and K share it, and so is the order of the output's entries, so a lane's 16-byte loads are the
-// operands of the matrix instructions as they are (K), or after one byte permutation that pairs
-// two tokens (V).  Lane 4 g + t:
-//   S (16 tokens x 8 heads) = K q^T: row g of K, entries 32 i + 8 t .. + 7 for k-steps 2 i, 2 i + 1
-//   O^T (128 x 8 heads) += V^T P: tokens 2t, 2t + 1, 2t + 8, 2t + 9, entries 8 g .. 8 g + 7 (+ 64)
-// P goes in as bf16 hi + lo (two products): rounding it to bf16 once would add as much error as
-// the rounding of the output.
-__global__ void __launch_bounds__(kThreads, kBlocksPerSM) attend_kernel(const __grid_constant__ Params p) {
-    extern __shared__ __align__(16) long long pre[];     // [batch + 1]
-    griddep_launch_dependents();
-    scan_tiles(p, pre);
+// A warp's walk over the tiles from cursor `ld` on; advance(c) moves a cursor to the next tile and says
+// whether it still belongs to the walk.  done(cu, ends, state) is called at the end of a unit (ends) or
+// of the walk, and the state starts afresh.
+//   S (16 tokens x 8 heads) = K q^T,   O^T (128 x 8 heads) += V^T P      (mma.sync, fp32 sums)
+// P goes in as bf16 hi + lo (two products): rounding it to bf16 once would add as much error as the
+// rounding of the output.  Rows past the sequence's end are not read; the copy writes zeros.
+// Loads are asynchronous copies of 512 contiguous bytes a warp (two rows): register loads in the
+// operand layout of K, 64 bytes of each of eight rows, stream a few per cent slower.
+template <typename Advance, typename Done>
+__device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Cursor ld, Advance advance, Done done) {
     const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
-    const int LK = p.layers * p.n_kv;
-    const long long total = pre[p.batch] * LK;
-    const long long most = total / kMinTiles;
-    const long long W = most < 1 ? 1 : most < p.warps ? most : p.warps;
-    // neighbouring runs go to different SMs, so that few runs spread over all of them
-    const long long w = (long long)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    if (w >= W) return;
-    const long long x0 = w * total / W, x1 = (w + 1) * total / W;
-    if (x0 >= x1) return;
-
-    Cursor ld{};
-    {
-        int lo = 0, hi = p.batch;                        // the sequence with pre[b] LK <= x0 < pre[b + 1] LK
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] * LK <= x0) lo = mid; else hi = mid;
-        }
-        ld.b = lo;
-        ld.nt = (int)(pre[lo + 1] - pre[lo]);
-        ld.len = clamped_len(p, lo, false);
-        const long long rem = x0 - pre[lo] * LK;
-        ld.lk = (int)(rem / ld.nt);
-        ld.t = (int)(rem % ld.nt);
-    }
     const int page_mask = (1 << p.page_shift) - 1;
-    auto advance = [&](Cursor &c) {
-        if (++c.t < c.nt) return;
-        c.t = 0;
-        if (++c.lk < LK) return;
-        c.lk = 0;
-        do ++c.b; while (c.b < p.batch && pre[c.b + 1] == pre[c.b]);
-        if (c.b < p.batch) {
-            c.nt = (int)(pre[c.b + 1] - pre[c.b]);
-            c.len = clamped_len(p, c.b, false);
-        }
-    };
+    const uint32_t sb = smem_u32(ring);
     auto page_of = [&](const Cursor &c) {
         return __ldg(p.table + (long long)c.b * p.max_pages + ((c.t * kTile) >> p.page_shift));
     };
-    // element offset of a tile's first row; n = its valid tokens (none where the page is out of range)
-    auto tile_at = [&](const Cursor &c, int page, int &n) {
-        n = min(kTile, c.len - c.t * kTile);
-        if (page < 0 || page >= p.n_pages) {
+    // copy of lane: row 2 i + lane / 16, chunk lane % 16, i < 8
+    const int row2 = lane >> 4, chunk = lane & 15;
+    uint32_t dst[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = (2 * i + row2) * 256 + ((chunk ^ ((2 * i + row2) & 7)) << 4);
+    auto fetch = [&](const Cursor &c, int page, int slot) {
+        int n = min(kTile, c.len - c.t * kTile);
+        if (page < 0 || page >= p.n_pages) {             // out of range: as if it held no tokens
             if (lane == 0) report_error(KVPACK_ERR_PAGE);
             n = 0;
             page = 0;
         }
         const int layer = c.lk / p.n_kv, kvh = c.lk - layer * p.n_kv;
-        return (((((long long)layer * p.n_pages + page) * p.n_kv + kvh) << p.page_shift) + ((c.t * kTile) & page_mask)) * 128;
-    };
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 kr[2][4], vr[4][2], qr[4];
-    auto load_k = [&](long long at, int n) {
+        const long long at =
+            (((((long long)layer * p.n_pages + page) * p.n_kv + kvh) << p.page_shift) + ((c.t * kTile) & page_mask)) * 128 +
+            row2 * 128 + chunk * 8;
+        const uint32_t to = sb + slot * kTileBytes;
         #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint16_t *src = p.K + at + (g + 8 * r) * 128 + 8 * tig;
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) kr[r][i] = g + 8 * r < n ? ldg_stream(src + 32 * i) : zero;
-        }
-    };
-    auto load_v = [&](long long at, int n) {
+        for (int i = 0; i < 8; ++i)
+            copy16(to + dst[i & 3] + (i >> 2) * 2048, p.K + at + i * 256, 2 * i + row2 < n);
         #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int tok = 2 * tig + (r & 1) + 8 * (r >> 1);
-            const uint16_t *src = p.V + at + tok * 128 + 8 * g;
-            #pragma unroll
-            for (int i = 0; i < 2; ++i) vr[r][i] = tok < n ? ldg_stream(src + 64 * i) : zero;
-        }
+        for (int i = 0; i < 8; ++i)
+            copy16(to + 4096 + dst[i & 3] + (i >> 2) * 2048, p.V + at + i * 256, 2 * i + row2 < n);
+        return n;
     };
 
-    Cursor cu = ld;                                      // the tile being computed; ld runs one ahead
-    int n_cu, n_ld = 0;
-    long long at_cu = tile_at(cu, page_of(cu), n_cu), at_ld = 0;
-    load_k(at_cu, n_cu);
-    int page_ld = 0;
-    advance(ld);
-    if (x0 + 1 < x1) page_ld = page_of(ld);
-
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, wt[8][4];
+    Cursor cu = ld;                                      // the tile being computed; ld runs kSlots - 1 ahead
+    int n[kSlots], ahead = 0;                            // tiles' valid rows; tiles fetched and not computed yet
+    int page_ld = page_of(ld);
+    bool more = true;                                    // ld is a tile of the walk
+    auto fetch_next = [&](int &nn, int slot) {
+        if (more) {
+            nn = fetch(ld, page_ld, slot);
+            ++ahead;
+            more = advance(ld);
+            if (more) page_ld = page_of(ld);
+        }
+        copy_commit();
+    };
     #pragma unroll
-    for (int e = 0; e < 8; ++e) wt[e][0] = wt[e][1] = wt[e][2] = wt[e][3] = 0.f;
+    for (int i = 0; i < kSlots; ++i) n[i] = 0;
+    #pragma unroll
+    for (int i = 0; i < kSlots - 1; ++i) fetch_next(n[i], i);
+    const int kx = (lane >> 4) ^ (lane & 7), vx = ((lane >> 3) & 1) ^ (lane & 7);
+    const uint32_t krow = (lane & 15) * 256, vrow = 4096 + ((lane & 7) + ((lane >> 4) << 3)) * 256;
+    State st;
+    st.clear();
+    uint32_t qf[8][2];
     bool fresh = true;                                   // q of cu's unit not loaded yet
-    bool head = cu.t != 0;                               // an earlier warp began cu's unit
 
-    for (long long x = x0; x < x1; ++x) {
-        const int layer = cu.lk / p.n_kv, kvh = cu.lk - layer * p.n_kv;
-        const long long lb = (long long)layer * p.batch + cu.b;
-        load_v(at_cu, n_cu);
+    auto step = [&](int slot, int &nt, int &nn) {
+        copy_wait<kSlots - 2>();                         // the tile has landed
+        __syncwarp();                                    // for every lane, and all are done with the one before
+        fetch_next(nn, (slot + kSlots - 1) % kSlots);
         if (fresh) {
-            const uint16_t *src = p.q + (lb * p.n_kv + kvh) * p.per_kv * 128 + (g < p.per_kv ? g : 0) * 128 + 8 * tig;
+            const int layer = cu.lk / p.n_kv, kvh = cu.lk - layer * p.n_kv;
+            const long long row = (((long long)layer * p.batch + cu.b) * p.n_kv + kvh) * p.per_kv;
+            const bool ok = g < p.per_kv;
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (row + (ok ? g : 0)) * 128) + tig;
             #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                qr[i] = g < p.per_kv ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * i)) : zero;
+            for (int k = 0; k < 8; ++k) {
+                qf[k][0] = ok ? __ldg(src + 8 * k) : 0u;
+                qf[k][1] = ok ? __ldg(src + 8 * k + 4) : 0u;
+            }
             fresh = false;
         }
+        const uint32_t tb = sb + slot * kTileBytes;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a0[4] = {kr[0][i].x, kr[1][i].x, kr[0][i].y, kr[1][i].y};
-            mma_bf16(s, a0, qr[i].x, qr[i].y);
-            const uint32_t a1[4] = {kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w};
-            mma_bf16(s, a1, qr[i].z, qr[i].w);
-        }
-        const int n = n_cu;
-        if (x + 1 < x1) {
-            at_ld = tile_at(ld, page_ld, n_ld);
-            load_k(at_ld, n_ld);
+        for (int k = 0; k < 8; ++k) {
+            uint32_t a[4];
+            ldsm_x4(tb + krow + (((2 * k) ^ kx) << 4), a[0], a[1], a[2], a[3]);
+            mma_bf16(s, a, qf[k][0], qf[k][1]);
         }
         // s[0], s[1]: token g, heads 2 tig, 2 tig + 1; s[2], s[3]: token g + 8
-        s[0] = g < n ? s[0] * p.scale2 : -INFINITY;
-        s[1] = g < n ? s[1] * p.scale2 : -INFINITY;
-        s[2] = g + 8 < n ? s[2] * p.scale2 : -INFINITY;
-        s[3] = g + 8 < n ? s[3] * p.scale2 : -INFINITY;
+        s[0] = g < nt ? s[0] * p.scale2 : -INFINITY;
+        s[1] = g < nt ? s[1] * p.scale2 : -INFINITY;
+        s[2] = g + 8 < nt ? s[2] * p.scale2 : -INFINITY;
+        s[3] = g + 8 < nt ? s[3] * p.scale2 : -INFINITY;
         float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
         #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
         }
-        const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
+        const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
         // no finite logit so far: exponents against 0, so that -inf - -inf does not appear
         const float r0 = mn0 == -INFINITY ? 0.f : mn0, r1 = mn1 == -INFINITY ? 0.f : mn1;
-        const float f0 = ex2(m[0] - r0), f1 = ex2(m[1] - r1);
+        const float f0 = ex2(st.m[0] - r0), f1 = ex2(st.m[1] - r1);
         const float p0 = ex2(s[0] - r0), p1 = ex2(s[1] - r1), p2 = ex2(s[2] - r0), p3 = ex2(s[3] - r1);
-        l[0] = l[0] * f0 + (p0 + p2);
-        l[1] = l[1] * f1 + (p1 + p3);
-        m[0] = mn0;
-        m[1] = mn1;
+        st.l[0] = st.l[0] * f0 + (p0 + p2);
+        st.l[1] = st.l[1] * f1 + (p1 + p3);
+        st.m[0] = mn0;
+        st.m[1] = mn1;
         uint32_t h0, h1, q0, q1;
         split2(p0, p1, h0, q0);
         split2(p2, p3, h1, q1);
@@ -236,137 +211,428 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) attend_kernel(const __
         q1 = movmatrix_t(q1);
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            wt[e][0] *= f0; wt[e][1] *= f1; wt[e][2] *= f0; wt[e][3] *= f1;
-            const uint32_t sel = e & 1 ? 0x7632u : 0x5410u;
-            const uint32_t a[4] = {__byte_perm(word(vr[0][0], e >> 1), word(vr[1][0], e >> 1), sel),
-                                   __byte_perm(word(vr[0][1], e >> 1), word(vr[1][1], e >> 1), sel),
-                                   __byte_perm(word(vr[2][0], e >> 1), word(vr[3][0], e >> 1), sel),
-                                   __byte_perm(word(vr[2][1], e >> 1), word(vr[3][1], e >> 1), sel)};
-            mma_bf16(wt[e], a, h0, h1);
-            mma_bf16(wt[e], a, q0, q1);
+            st.o[e][0] *= f0; st.o[e][1] *= f1; st.o[e][2] *= f0; st.o[e][3] *= f1;
+            uint32_t a[4];
+            ldsm_x4_t(tb + vrow + (((2 * e) ^ vx) << 4), a[0], a[1], a[2], a[3]);
+            mma_bf16(st.o[e], a, h0, h1);
+            mma_bf16(st.o[e], a, q0, q1);
         }
-
+        --ahead;
         const bool ends = cu.t + 1 == cu.nt;             // the unit ends with this tile
-        if (ends || x + 1 == x1) {
-            #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
-            const long long row = (lb * p.n_kv + kvh) * p.per_kv;
-            const bool whole = ends && !head;
-            if (!head && lane == 0) {                    // this warp began the unit: where its parts are
-                const long long last = x + (cu.nt - 1 - cu.t);
-                const long long w1 = ((last + 1) * W - 1) / total;
-                p.desc[lb * p.n_kv + kvh] = make_int2((int)w, (int)(w1 - w) + 1);
+        if (ends || ahead == 0) {
+            st.sum_lanes();
+            done(cu, ends, st);
+            st.clear();
+            fresh = true;
+        }
+        if (ahead > 0) advance(cu);
+    };
+    while (ahead > 0) {
+        #pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            if (ahead > 0) step(i, n[i], n[(i + kSlots - 1) % kSlots]);
+    }
+}
+
+// 64-bit quotient; the 32-bit division is several times faster, and enough for nearly all
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The places, `total` of them, in runs: the first W0 share `cut` places, the other W1 the rest, each evenly
+// (the first `more` of a share have one place more).  The second share's runs are the shorter ones: they
+// go to the SMs that have finished runs of the first.
+struct Runs {
+    long long W0, W, cut, base0, more0, base1, more1;
+
+    __device__ __forceinline__ Runs(long long total, int slots) {
+        const long long most = total / kMinPlaces;
+        W0 = most < 1 ? 1 : most < slots ? most : slots;
+        const bool two = total >= W0 * kTwoShares;
+        const long long W1 = two ? W0 * kSecond : 0;
+        cut = two ? total * kCut / 16 : total;
+        W = W0 + W1;
+        base0 = quotient(cut, W0);
+        more0 = cut - base0 * W0;
+        base1 = two ? quotient(total - cut, W1) : 0;
+        more1 = total - cut - base1 * W1;
+    }
+    __device__ __forceinline__ long long first(long long w) const {
+        if (w <= W0) return w * base0 + (w < more0 ? w : more0);
+        w -= W0;
+        return cut + w * base1 + (w < more1 ? w : more1);
+    }
+    __device__ __forceinline__ long long of(long long x) const {
+        const long long base = x < cut ? base0 : base1, more = x < cut ? more0 : more1;
+        const long long y = x < cut ? x : x - cut, w = x < cut ? 0 : W0, longer = more * (base + 1);
+        return w + (y < longer ? quotient(y, base + 1) : more + quotient(y - longer, base));
+    }
+};
+
+// -------------------------------------------------------------------------- runs over all units
+
+__device__ __forceinline__ long long warp_sums(long long v, int lane) {
+    #pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Places of all sequences, in the sequences' order, by a warp.  A unit of nt tiles has nt + 1 places: its
+// end costs about as much as a tile (the queries' load, the sums over lanes, the output), so that runs of
+// short units would end late if only tiles counted.  Lane i has the places of the `per` groups of 32
+// sequences from i * per on, and the sum up to their end.
+struct Lengths {
+    const Params &p;
+    int lane, per;
+    long long mine, upto, total;     // total: of one layer and KV head
+
+    __device__ __forceinline__ int places_of(int b) const {
+        const int len = b < p.batch ? clamped_len(p, b, false) : 0;
+        return len > 0 ? (len + kTile - 1) / kTile + 1 : 0;
+    }
+    __device__ __forceinline__ Lengths(const Params &p_, int lane_) : p(p_), lane(lane_) {
+        const int groups = (p.batch + 31) / 32;
+        per = (groups + 31) / 32;
+        mine = 0;
+        #pragma unroll 8
+        for (int i = 0; i < groups; ++i) {
+            const unsigned sum = __reduce_add_sync(0xffffffffu, (unsigned)places_of(32 * i + lane));
+            if (i / per == lane) mine += sum;
+        }
+        upto = warp_sums(mine, lane);
+        total = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    // the sequence whose places, times LK, hold place x: b, its places, and those before it
+    __device__ __forceinline__ void find(long long x, int LK, int &b, int &own, long long &before) const {
+        const int at = __popc(__ballot_sync(0xffffffffu, upto * LK <= x));
+        before = __shfl_sync(0xffffffffu, upto - mine, at);
+        b = own = 0;
+        for (int i = at * per; i < (at + 1) * per; ++i) {
+            const long long t = places_of(32 * i + lane), end = before + warp_sums(t, lane);
+            const uint32_t past = __ballot_sync(0xffffffffu, end * LK > x);
+            if (past != 0) {
+                const int s = __ffs(past) - 1;
+                b = 32 * i + s;
+                own = (int)__shfl_sync(0xffffffffu, t, s);
+                before = __shfl_sync(0xffffffffu, end, s) - own;
+                return;
             }
+            before = __shfl_sync(0xffffffffu, end, 31);
+        }
+    }
+    // places before sequence b
+    __device__ __forceinline__ long long before(int b) const {
+        const int at = b / (32 * per);
+        long long n = __shfl_sync(0xffffffffu, upto - mine, at);
+        for (int i = at * per; 32 * i < b; ++i)
+            n += __reduce_add_sync(0xffffffffu, (unsigned)(32 * i + lane < b ? places_of(32 * i + lane) : 0));
+        return n;
+    }
+};
+
+// A block is one warp and takes one run.  The runs of the first share fill the GPU; those of the
+// second go where an SM is done, since SMs do not get equal parts of the memory's bandwidth (with equal
+// shares for all, the last warp ended 15 % after the median).
+__global__ void __launch_bounds__(32) attend_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    // in this order: the join may then read the lengths, which a kernel before this one may write
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x, g = lane >> 2, tig = lane & 3;
+    const int LK = p.layers * p.n_kv;
+    const Lengths lens(p, lane);
+    const long long total = lens.total * LK, w = blockIdx.x;   // places
+    if (blockIdx.x == 0)
+        for (int b = lane; b < p.batch; b += 32) clamped_len(p, b, true);
+    if (total == 0) return;
+    const Runs runs(total, p.slots);
+    if (w >= runs.W) return;
+    const long long x0 = runs.first(w), x1 = runs.first(w + 1);
+
+    auto advance = [&](Cursor &c) {
+        ++c.x;
+        if (++c.t < c.nt) return c.x < x1;
+        if (++c.x >= x1) return false;                   // past the unit's last place
+        c.t = 0;
+        if (++c.lk < LK) return true;
+        c.lk = 0;
+        do c.len = clamped_len(p, ++c.b, false); while (c.len == 0);   // x < total: there is one
+        c.nt = (c.len + kTile - 1) / kTile;
+        return true;
+    };
+    Cursor first{};
+    {
+        long long before;
+        int own;
+        lens.find(x0, LK, first.b, own, before);
+        first.x = x0;
+        first.nt = own - 1;
+        first.len = clamped_len(p, first.b, false);
+        const long long rem = x0 - before * LK;
+        first.lk = (int)quotient(rem, own);
+        first.t = (int)(rem - (long long)first.lk * own);
+        if (first.t == first.nt) {                       // the place that has no tile: on to the next unit
+            --first.t;
+            --first.x;
+            if (!advance(first)) return;
+        }
+    }
+    bool head = first.t != 0;                            // an earlier run began the current unit
+    walk(p, smem, first, advance, [&](const Cursor &cu, bool ends, const State &st) {
+        const int layer = cu.lk / p.n_kv, kvh = cu.lk - layer * p.n_kv;
+        const long long unit = ((long long)layer * p.batch + cu.b) * p.n_kv + kvh, row = unit * p.per_kv;
+        const bool whole = ends && !head;
+        #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int hh = 2 * tig + e;
+            if (hh >= p.per_kv) continue;
+            if (whole && p.tpart == nullptr) {
+                if (p.lse != nullptr && g == 0) p.lse[row + hh] = (st.m[e] + log2f(st.l[e])) * kLn2;
+            } else {
+                const long long slot = 2 * w + (head ? 0 : 1);
+                float *ml = whole ? p.tpart + (row + hh) * decode::kTxtPart : p.stat + (slot * 8 + hh) * 2;
+                if (g == 0) *reinterpret_cast<float2 *>(ml) = make_float2(st.m[e], st.l[e]);
+                st.store(e, g, whole ? ml + 2 : p.acc + (slot * p.per_kv + hh) * 128);
+            }
+        }
+        if (whole && p.tpart == nullptr) {
+            // transposed: lane 4 g + t has entries 8 c + 2 t, + 1 of head g
+            const float i0 = 1.f / st.l[0], i1 = 1.f / st.l[1];
+            uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row + g) * 128) + tig;
+            #pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t v = movmatrix_t(pack_bf16(st.o[c >> 1][2 * (c & 1)] * i0, st.o[c >> 1][2 * (c & 1) + 1] * i1));
+                if (g < p.per_kv) dst[4 * c] = v;
+            }
+        }
+        head = false;
+    });
+}
+
+// What a joined row (unit, head) becomes: M and L of all its tokens, v = entry tid of sum 2^(s - M) V
+__device__ __forceinline__ void write_row(const Params &p, long long row, bool none, float M, float L, float4 v, int lane) {
+    if (p.tpart != nullptr) {
+        float *dst = p.tpart + row * decode::kTxtPart;
+        if (lane == 0) *reinterpret_cast<float2 *>(dst) = make_float2(M, L);
+        *reinterpret_cast<float2 *>(dst + 2 + 4 * lane) = make_float2(v.x, v.y);
+        *reinterpret_cast<float2 *>(dst + 4 + 4 * lane) = make_float2(v.z, v.w);
+        return;
+    }
+    const float il = none ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2 *>(p.out + row * 128 + 4 * lane) =
+        make_uint2(pack_bf16(v.x * il, v.y * il), pack_bf16(v.z * il, v.w * il));
+    if (p.lse != nullptr && lane == 0) p.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// The parts of the units that several runs share, in their order,
+//   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k,
+// and the rows of sequences without tokens (out 0, lse -inf).  JW warps take a row (unit, query head),
+// and with JW = 1 a warp takes rows in turn.  Where a unit's parts are follows from the lengths: the
+// sums over them are taken while the attention still runs.
+template <int JW>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p, long long rows) {
+    constexpr int kAhead = 4;                            // parts a warp loads at a time
+    __shared__ float4 red[JW > 1 ? 8 : 1][32];
+    __shared__ float ml[8][2];
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jw = warp % JW;
+    const int LK = p.layers * p.n_kv;
+    // the lengths are inputs, complete when attend_kernel let this kernel start
+    const Lengths lens(p, lane);
+    const Runs runs(lens.total > 0 ? lens.total * LK : 1, p.slots);
+    bool waited = false;
+    for (long long row = (long long)blockIdx.x * (8 / JW) + warp / JW; row < rows || (JW > 1 && !waited);
+         row += (long long)gridDim.x * (8 / JW)) {
+        const bool in = row < rows;
+        const long long unit = quotient(in ? row : 0, p.per_kv), lb = quotient(unit, p.n_kv);
+        const int hh = (int)(row - unit * p.per_kv);
+        const int layer = (int)quotient(lb, p.batch), b = (int)(lb - (long long)layer * p.batch);
+        const int len = clamped_len(p, b, false), nt = (len + kTile - 1) / kTile;
+        int parts = 0;
+        long long w0 = 0;
+        if (in && len > 0) {
+            const long long x = lens.before(b) * LK + (layer * p.n_kv + (unit - lb * p.n_kv)) * (nt + 1);
+            w0 = runs.of(x);
+            parts = (int)(runs.of(x + nt - 1) - w0) + 1;
+        }
+        if (!waited) griddep_wait();
+        waited = true;
+        if (JW == 1 && parts == 1) continue;             // its warp finished it
+        auto slot = [&](int k) { return k == 0 ? 2 * w0 + 1 : 2 * (w0 + k); };
+        float M = -INFINITY, L = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = jw; k0 < parts && parts > 1; k0 += JW * kAhead) {
+            float2 st[kAhead];
+            float4 c[kAhead];
+            float top = M;
+            #pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = k0 + i * JW;
+                st[i] = make_float2(-INFINITY, 0.f);
+                c[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < parts) {
+                    st[i] = *reinterpret_cast<const float2 *>(p.stat + (slot(k) * 8 + hh) * 2);
+                    c[i] = *reinterpret_cast<const float4 *>(p.acc + (slot(k) * p.per_kv + hh) * 128 + 4 * lane);
+                }
+                top = fmaxf(top, st[i].x);
+            }
+            const float R = top == -INFINITY ? 0.f : top, f = ex2(M - R);
+            L *= f;
+            a.x *= f; a.y *= f; a.z *= f; a.w *= f;
+            M = top;
+            #pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float f = ex2(st[i].x - R);
+                L = fmaf(st[i].y, f, L);
+                a.x = fmaf(c[i].x, f, a.x);
+                a.y = fmaf(c[i].y, f, a.y);
+                a.z = fmaf(c[i].z, f, a.z);
+                a.w = fmaf(c[i].w, f, a.w);
+            }
+        }
+        if constexpr (JW > 1) {
+            red[warp][lane] = a;
+            if (lane == 0) { ml[warp][0] = M; ml[warp][1] = L; }
+            __syncthreads();
+            if (jw != 0) return;                         // one row a block
+            const float own = M;
+            #pragma unroll
+            for (int i = 1; i < JW; ++i) M = fmaxf(M, ml[warp + i][0]);
+            const float R = M == -INFINITY ? 0.f : M, f = ex2(own - R);
+            L *= f;
+            a.x *= f; a.y *= f; a.z *= f; a.w *= f;
+            #pragma unroll
+            for (int i = 1; i < JW; ++i) {
+                const float f = ex2(ml[warp + i][0] - R);
+                const float4 c = red[warp + i][lane];
+                L = fmaf(ml[warp + i][1], f, L);
+                a.x = fmaf(c.x, f, a.x);
+                a.y = fmaf(c.y, f, a.y);
+                a.z = fmaf(c.z, f, a.z);
+                a.w = fmaf(c.w, f, a.w);
+            }
+        }
+        if (in && parts != 1) write_row(p, row, len <= 0, M, L, a, lane);
+        if (JW > 1) return;
+    }
+    if (!waited) griddep_wait();
+}
+
+// ------------------------------------------------------------------ a cluster of blocks per unit
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// Short caches of few units: a cluster takes one unit, its warps equal shares of the unit's tiles,
+// and the parts meet in the blocks' shared memories.  One launch, nothing to scan, no workspace.
+__global__ void __launch_bounds__(kThreads, kUnitBlocksPerSM) unit_kernel(const __grid_constant__ Params p, int S) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ __align__(16) float2 pml[kWarps][8];
+    __shared__ __align__(16) float sum[8][128];
+    __shared__ __align__(16) float2 ml[8];
+    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
+    const int rank = (int)(blockIdx.x % S);
+    const long long unit = blockIdx.x / S;
+    const long long lb = unit / p.n_kv;
+    const int layer = (int)(lb / p.batch), b = (int)(lb - (long long)layer * p.batch), kvh = (int)(unit - lb * p.n_kv);
+    griddep_wait();
+    const int len = clamped_len(p, b, blockIdx.x % S == 0);
+    const long long row = unit * p.per_kv;
+    if (len == 0) {                                      // the same for the whole cluster
+        if (rank == 0)
+            for (int h = warp; h < p.per_kv; h += kWarps)
+                write_row(p, row + h, true, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), lane);
+        return;
+    }
+    const int nt = (len + kTile - 1) / kTile, n_warps = S * kWarps, w = rank * kWarps + warp;
+    const int base = nt / n_warps, more = nt - base * n_warps;
+    const int t0 = w * base + min(w, more), count = base + (w < more ? 1 : 0);
+    unsigned char *ring = smem + warp * kRingBytes;
+    if (count > 0) {
+        const Cursor first{b, layer * p.n_kv + kvh, t0, nt, len, 0};
+        walk(p, ring, first, [&](Cursor &c) { return ++c.t < t0 + count; }, [&](const Cursor &, bool, const State &st) {
+            __syncwarp();                                // the ring has been read: the part goes there
             #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int hh = 2 * tig + e;
                 if (hh >= p.per_kv) continue;
-                if (whole && p.tpart == nullptr) {
-                    const float il = 1.f / l[e];
-                    uint32_t o[2][4];
-                    #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[i][k] = pack_bf16(wt[2 * k][2 * i + e] * il, wt[2 * k + 1][2 * i + e] * il);
-                    uint16_t *dst = p.out + (row + hh) * 128 + 8 * g;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-                    *reinterpret_cast<uint4 *>(dst + 64) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-                    if (p.lse != nullptr && g == 0) p.lse[row + hh] = (m[e] + log2f(l[e])) * kLn2;
-                } else {
-                    const long long slot = 2 * w + (head ? 0 : 1);
-                    float *st = whole ? p.tpart + (row + hh) * decode::kTxtPart : p.stat + (slot * 8 + hh) * 2;
-                    float *dst = whole ? st + 2 : p.acc + (slot * p.per_kv + hh) * 128;
-                    if (g == 0) *reinterpret_cast<float2 *>(st) = make_float2(m[e], l[e]);
-                    #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<float2 *>(dst + 64 * i + 8 * g + 2 * k) =
-                                make_float2(wt[2 * k][2 * i + e], wt[2 * k + 1][2 * i + e]);
-                }
+                if (g == 0) pml[warp][hh] = make_float2(st.m[e], st.l[e]);
+                st.store(e, g, reinterpret_cast<float *>(ring) + hh * 128);
             }
-            m[0] = m[1] = -INFINITY;
-            l[0] = l[1] = 0.f;
-            #pragma unroll
-            for (int e = 0; e < 8; ++e) wt[e][0] = wt[e][1] = wt[e][2] = wt[e][3] = 0.f;
-            head = false;
-            fresh = true;
-        }
-        cu = ld;
-        at_cu = at_ld;
-        n_cu = n_ld;
-        if (x + 2 < x1) {
-            advance(ld);
-            page_ld = page_of(ld);
-        }
+        });
     }
-}
-
-// One block per (unit, query head): the parts of a unit that several warps share, in their order,
-//   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k,
-// and the rows of sequences without tokens (out 0, lse -inf).
-constexpr int kJoinWarps = 8;
-
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ Params p) {
-    __shared__ float red[kJoinWarps][128];
-    __shared__ float ml[kJoinWarps][2];
-    griddep_wait();
-    const int hh = blockIdx.x % p.per_kv;
-    const long long unit = blockIdx.x / p.per_kv;
-    const int b = (int)((unit / p.n_kv) % p.batch);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long row = unit * p.per_kv + hh;
-    float M = -INFINITY, L = 0.f, v = 0.f;
-    if (__ldg(p.lens + b) > 0) {
-        const int2 d = p.desc[unit];
-        if (d.y == 1) return;                            // its warp finished it
-        auto slot = [&](int k) { return k == 0 ? 2LL * d.x + 1 : 2LL * (d.x + k); };
-        for (int k = tid; k < d.y; k += kJoinWarps * 32) M = fmaxf(M, p.stat[(slot(k) * 8 + hh) * 2]);
-        #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        if (lane == 0) ml[warp][0] = M;
-        __syncthreads();
-        #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, ml[i][0]);
-        const float R = M == -INFINITY ? 0.f : M;
+    __syncthreads();
+    // the block's parts, in the warps' order (warps without tiles are the last ones)
+    const int live = base > 0 ? kWarps : max(0, min(kWarps, nt - rank * kWarps));
+    for (int h = warp; h < p.per_kv; h += kWarps) {
+        float M = -INFINITY, L = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lw = 0.f;
-        #pragma unroll 4
-        for (int k = warp; k < d.y; k += kJoinWarps) {
-            const long long s = slot(k);
-            const float2 st = *reinterpret_cast<const float2 *>(p.stat + (s * 8 + hh) * 2);
-            const float f = ex2(st.x - R);
-            const float4 c = *reinterpret_cast<const float4 *>(p.acc + (s * p.per_kv + hh) * 128 + 4 * lane);
-            lw = fmaf(st.y, f, lw);
+        for (int i = 0; i < live; ++i) M = fmaxf(M, pml[i][h].x);
+        const float R = M == -INFINITY ? 0.f : M;
+        for (int i = 0; i < live; ++i) {
+            const float f = ex2(pml[i][h].x - R);
+            const float4 c = *reinterpret_cast<const float4 *>(smem + i * kRingBytes + h * 512 + 16 * lane);
+            L = fmaf(pml[i][h].y, f, L);
             a.x = fmaf(c.x, f, a.x);
             a.y = fmaf(c.y, f, a.y);
             a.z = fmaf(c.z, f, a.z);
             a.w = fmaf(c.w, f, a.w);
         }
-        *reinterpret_cast<float4 *>(&red[warp][4 * lane]) = a;
-        if (lane == 0) ml[warp][1] = lw;
-        __syncthreads();
-        if (tid < 128) {
-            #pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) {
-                v += red[i][tid];
-                L += ml[i][1];
+        *reinterpret_cast<float4 *>(&sum[h][4 * lane]) = a;
+        if (lane == 0) ml[h] = make_float2(M, L);
+    }
+    cluster_arrive();
+    cluster_wait();
+    // head h of the unit is joined by warp h / S of block h % S
+    for (int h = warp * S + rank; h < p.per_kv; h += kWarps * S) {
+        const uint32_t at = smem_u32(&sum[h][4 * lane]), at_ml = smem_u32(&ml[h]);
+        float M = -INFINITY, L = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 st[kMaxCluster];
+        float4 c[kMaxCluster];
+        #pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+            if (i < S) {
+                st[i] = cluster_ld2(cluster_map(at_ml, i));
+                c[i] = cluster_ld4(cluster_map(at, i));
+                M = fmaxf(M, st[i].x);
             }
-        }
+        const float R = M == -INFINITY ? 0.f : M;
+        #pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i)
+            if (i < S) {
+                const float f = ex2(st[i].x - R);
+                L = fmaf(st[i].y, f, L);
+                a.x = fmaf(c[i].x, f, a.x);
+                a.y = fmaf(c[i].y, f, a.y);
+                a.z = fmaf(c[i].z, f, a.z);
+                a.w = fmaf(c[i].w, f, a.w);
+            }
+        write_row(p, row + h, false, M, L, a, lane);
     }
-    if (tid >= 128) return;
-    if (p.tpart != nullptr) {
-        float *dst = p.tpart + row * decode::kTxtPart;
-        if (tid == 0) { dst[0] = M; dst[1] = L; }
-        dst[2 + tid] = v;
-        return;
-    }
-    const bool none = __ldg(p.lens + b) <= 0;
-    p.out[row * 128 + tid] = float_to_bf16_bits(none ? 0.f : v / L);
-    if (p.lse != nullptr && tid == 0) p.lse[row] = (M + log2f(L)) * kLn2;
+    cluster_arrive();                                    // no block leaves while another reads its sums
+    cluster_wait();
 }
 
 }  // namespace paged

@@ -111,6 +111,8 @@ constexpr int kThreads = 256;
 template <bool APPEND, bool ADJ>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
     constexpr int U = 4;                        // quads in flight
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31, c = lane & 7, sub = lane >> 3;
     const long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (item >= p.items) return;

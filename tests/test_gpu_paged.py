@@ -22,10 +22,10 @@ def _attend(kv, dims, layers, q, K, V, table, lens, scale, want_lse=True):
     return out, lse
 
 
-def _case(seed, layers, lens, n_q, n_kv, page, qscale=2.0, fill=float("nan"), behind=-1):
+def _case(seed, layers, lens, n_q, n_kv, page, qscale=2.0, fill=float("nan"), behind=-1, wide=2):
     import rank_compressed_kv_b200 as kv
     g = torch.Generator().manual_seed(seed)
-    table, n_pages = pages_for(lens, page, g, behind=behind)
+    table, n_pages = pages_for(lens, page, g, behind=behind, wide=wide)
     K, V = normal(g, layers, n_pages, n_kv, page, D), normal(g, layers, n_pages, n_kv, page, D)
     if fill is not None:
         blank_unused(K, table, lens, page, fill)
@@ -39,6 +39,10 @@ def _dev(*ts):
     return [t.to(DEV) for t in ts]
 
 
+WIDE = [2, 1000]      # spare columns of the table: the attention takes another form where it could hold long caches
+
+
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("layers,lens,n_q,n_kv,page", [
     (1, [1], 8, 8, 16),
     (1, [16], 8, 1, 16),
@@ -53,9 +57,9 @@ def _dev(*ts):
     (1, [(37 * i) % 211 for i in range(130)], 24, 4, 16),
     (2, [33] * 64, 8, 8, 32),
 ])
-def test_attend_matches_fp64(layers, lens, n_q, n_kv, page):
+def test_attend_matches_fp64(layers, lens, n_q, n_kv, page, wide):
     """Slots that hold no token are NaN, table entries behind the last page out of range."""
-    kv, dims, q, K, V, table = _case(len(lens) * 100 + n_q, layers, lens, n_q, n_kv, page, behind=2 ** 31 - 1)
+    kv, dims, q, K, V, table = _case(len(lens) * 100 + n_q, layers, lens, n_q, n_kv, page, behind=2 ** 31 - 1, wide=wide)
     scale = D ** -0.5
     ln = torch.tensor(lens, dtype=torch.int32)
     d = _dev(q, K, V, table, ln)
@@ -68,10 +72,11 @@ def test_attend_matches_fp64(layers, lens, n_q, n_kv, page):
     assert torch.equal(out, only)
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("per", range(1, 9))
-def test_every_number_of_query_heads_per_cached_head(per):
+def test_every_number_of_query_heads_per_cached_head(per, wide):
     lens = [70, 2000, 19]
-    kv, dims, q, K, V, table = _case(per, 1, lens, 2 * per, 2, 32)
+    kv, dims, q, K, V, table = _case(per, 1, lens, 2 * per, 2, 32, wide=wide)
     out, lse = _attend(kv, dims, 1, *_dev(q, K, V, table, torch.tensor(lens, dtype=torch.int32)), 0.1)
     close_attend(out.cpu(), lse.cpu(), attend(q, K, V, table, lens, 32, 0.1))
 
@@ -99,10 +104,11 @@ def test_distributions(what):
     close_attend(out.cpu(), lse.cpu(), attend(q, K, V, table, lens, 64, D ** -0.5))
 
 
-def test_infinite_and_nan_values_follow_the_formula():
+@pytest.mark.parametrize("wide", WIDE)
+def test_infinite_and_nan_values_follow_the_formula(wide):
     """Logits of -inf weigh nothing (all of a row: NaN, as 0 / 0); a NaN or +inf logit makes its heads NaN."""
     lens = [100, 100, 100, 100]
-    kv, dims, q, K, V, table = _case(4, 1, lens, 4, 4, 16, fill=None)
+    kv, dims, q, K, V, table = _case(4, 1, lens, 4, 4, 16, fill=None, wide=wide)
     q[:, :, 0] = 1.0
     t = torch.arange(100)
 
@@ -160,9 +166,10 @@ def test_pools_beyond_32_bits():
     assert kv.last_device_status() == 0
 
 
-def test_a_replayed_graph_follows_the_lengths_and_two_graphs_have_workspaces_of_their_own():
+@pytest.mark.parametrize("wide", WIDE)
+def test_a_replayed_graph_follows_the_lengths_and_two_graphs_have_workspaces_of_their_own(wide):
     lens = [900, 20, 333]
-    kv, dims, q, K, V, table = _case(21, 1, lens, 16, 4, 32, fill=None)
+    kv, dims, q, K, V, table = _case(21, 1, lens, 16, 4, 32, fill=None, wide=wide)
     qd, Kd, Vd, td, ln = _dev(q, K, V, table, torch.tensor(lens, dtype=torch.int32))
     sides = [torch.cuda.Stream() for _ in range(2)]
     graphs, outs = [], []
@@ -187,10 +194,11 @@ def test_a_replayed_graph_follows_the_lengths_and_two_graphs_have_workspaces_of_
             close_attend(o.cpu(), l.cpu(), ref)
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("what", ["length", "negative length", "page", "negative page"])
-def test_lengths_and_pages_out_of_range_are_reported(what):
+def test_lengths_and_pages_out_of_range_are_reported(what, wide):
     lens = [200, 40]
-    kv, dims, q, K, V, table = _case(2, 1, lens, 8, 4, 16, fill=None)
+    kv, dims, q, K, V, table = _case(2, 1, lens, 8, 4, 16, fill=None, wide=wide)
     ln = torch.tensor(lens, dtype=torch.int32)
     if what == "length":
         table[1] = 0
@@ -389,7 +397,8 @@ def _paged_tail(c, w, n_layers, lens, page, seed):
 
 @pytest.mark.parametrize("batch,layers,n_q,n_kv,T,lens,rank_lo", [
     (2, 2, 8, 8, 300, [45, 45], 16), (3, 1, 32, 8, 700, [0, 1, 130], 16), (2, 1, 28, 4, 1500, [17, 1000], 16),
-    (2, 1, 32, 4, 600, [64, 0], 0), (1, 1, 8, 8, 64, [0], 16)])
+    (2, 1, 32, 4, 600, [64, 0], 0), (1, 1, 8, 8, 64, [0], 16),
+    (2, 1, 16, 8, 200, [5000, 77], 16)])
 def test_decode_with_a_paged_text_tail_matches_the_oracle(batch, layers, n_q, n_kv, T, lens, rank_lo):
     import rank_compressed_kv_b200 as kv
     w = synth.Workload("paged", 50 + T, batch, layers, n_q, n_kv, T, max(max(lens), 1), 1, "lowrank32")
