@@ -1122,19 +1122,29 @@ void set_spec(rp::Params &p, const kvpack_rope_spec *r, const double *freq, cons
     for (int i = 0; i < r->rotary_dim / 2; ++i) p.axis2[i >> 4] |= (uint32_t)r->axis[i] << (2 * (i & 15));
 }
 
-// Splits of a row's heads over warps: one warp per row where the rows alone fill the GPU.
+template <bool APPEND, int U>
+cudaError_t launch_rope_u(const rp::Params &p, long long grid, bool adjacent, cudaStream_t st) {
+    return adjacent ? launch_pdl(rp::rope_kernel<APPEND, true, U>, (int)grid, rp::kThreads, 0, st, p)
+                    : launch_pdl(rp::rope_kernel<APPEND, false, U>, (int)grid, rp::kThreads, 0, st, p);
+}
+
+// Few rows: a row's quads split over as many warps as the GPU holds, two loaded at a time (576 rows of 64
+// heads 4.0 us; 4.2 with three, 4.7 with four).  Many rows: a warp each, and more on the way: four quads
+// in the rotation (100352 rows of 32 heads 247 us; 258 with three, 263 with two), three in the append,
+// whose stores scatter (53 k rows of 36 heads 151 us; 155 with two, 162 with four), less for few heads.
 template <bool APPEND>
 kvpack_status launch_rope(rp::Params &p, long long orows, bool adjacent, cudaStream_t st) {
-    const long long want = (long long)kPlanSMs * 32;
-    const long long splits = (want + orows - 1) / orows;
+    const long long splits = (long long)kPlanSMs * rp::kWarpsPerSM / orows;
     p.splits = (int)(splits < 1 ? 1 : splits > p.quads ? p.quads : splits);
     p.qpw = (p.quads + p.splits - 1) / p.splits;
     p.splits = (p.quads + p.qpw - 1) / p.qpw;
     p.items = orows * p.splits;
     const long long grid = (p.items + rp::kThreads / 32 - 1) / (rp::kThreads / 32);
     if (grid > 0x7fffffffLL) return KVPACK_ERR_UNSUPPORTED;
-    const cudaError_t e = adjacent ? launch_pdl(rp::rope_kernel<APPEND, true>, (int)grid, rp::kThreads, 0, st, p)
-                                   : launch_pdl(rp::rope_kernel<APPEND, false>, (int)grid, rp::kThreads, 0, st, p);
+    cudaError_t e;
+    if (p.splits > 1 || (APPEND && p.quads < 6)) e = launch_rope_u<APPEND, 2>(p, grid, adjacent, st);
+    else if (APPEND || p.quads < 4) e = launch_rope_u<APPEND, 3>(p, grid, adjacent, st);
+    else e = launch_rope_u<APPEND, APPEND ? 3 : 4>(p, grid, adjacent, st);
     return e == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
 }
 

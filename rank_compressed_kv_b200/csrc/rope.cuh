@@ -103,14 +103,17 @@ __device__ __forceinline__ void turn(uint4 &a, uint4 &b, const float (&c)[8], co
     b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kBlocks = 8;          // per SM: 64 registers a thread
+constexpr int kWarpsPerSM = kBlocks * kThreads / 32;
 
 // A warp takes a row's heads (or a share of them) four at a time: lane 8 s + c holds head s of the
 // four and two 16-byte chunks of it, for c < R/16 the two halves of pairs 8c .. 8c + 7.  A lane
 // evaluates two of the row's angles; the eight it needs come from the four lanes of the same c.
-template <bool APPEND, bool ADJ>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
-    constexpr int U = 4;                        // quads in flight
+// U quads are loaded at a time, the first before the angles are worked out.  Memory bounds long calls:
+// 16 x 6272 rows of 32 heads move 1.65 GB in 247 us (a plain copy of as much takes 251).
+template <bool APPEND, bool ADJ, int U>
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ Params p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, c = lane & 7, sub = lane >> 3;
@@ -123,6 +126,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const bool rotated = c < p.rot8;
     const int e0 = ADJ ? 16 * c : rotated ? 8 * c : 16 * c;
     const int e1 = ADJ ? e0 + 8 : rotated ? 8 * (p.rot8 + c) : e0 + 8;
+
+    // the quad's tensor (0 q, 1 k, 2 v) and its number in it
+    auto part = [&](int qd, int &g) {
+        const int t = qd < p.quads_q ? 0 : !APPEND || qd < p.quads_q + p.quads_k ? 1 : 2;
+        g = qd - (t == 0 ? 0 : t == 1 ? p.quads_q : p.quads_q + p.quads_k);
+        return t;
+    };
+    uint4 a[U], b[U];
+    auto load = [&](int qd0) {
+        #pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int g;
+            const int t = part(qd0 + u, g);
+            const View &s = t == 0 ? p.q : t == 1 ? p.k : p.v;
+            if (qd0 + u < q1 && 4 * g + sub < (t == 0 ? p.n_q : p.n_k)) {
+                const uint16_t *src = s.data + outer * s.outer + row * s.row + g * s.group + sub * 128;
+                a[u] = *reinterpret_cast<const uint4 *>(src + e0);
+                b[u] = *reinterpret_cast<const uint4 *>(src + e1);
+            }
+        }
+    };
+    load(q0);                                   // on their way while the angles and the slot are worked out
 
     bool found = true;
     int page = 0, at = 0;
@@ -154,33 +179,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
 
     for (int qd0 = q0; qd0 < q1; qd0 += U) {
-        uint4 a[U], b[U];
+        if (qd0 > q0) load(qd0);
         #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int qd = qd0 + u;
-            const bool is_q = qd < p.quads_q, is_k = !is_q && qd < p.quads_q + p.quads_k;
-            const int g = is_q ? qd : is_k ? qd - p.quads_q : qd - p.quads_q - p.quads_k;
-            const View &s = is_q ? p.q : is_k || !APPEND ? p.k : p.v;
-            if (qd < q1 && 4 * g + sub < (is_q ? p.n_q : p.n_k)) {
-                const uint16_t *src = s.data + outer * s.outer + row * s.row + g * s.group + sub * 128;
-                a[u] = *reinterpret_cast<const uint4 *>(src + e0);
-                b[u] = *reinterpret_cast<const uint4 *>(src + e1);
-            }
-        }
-        #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int qd = qd0 + u;
-            const bool is_q = qd < p.quads_q, is_k = !is_q && qd < p.quads_q + p.quads_k;
-            const int g = is_q ? qd : is_k ? qd - p.quads_q : qd - p.quads_q - p.quads_k;
-            const int h = 4 * g + sub;
-            if (qd < q1 && h < (is_q ? p.n_q : p.n_k)) {
-                if (rotated && (is_q || is_k)) turn<ADJ>(a[u], b[u], cs, sn);
+            int g;
+            const int t = part(qd0 + u, g), h = 4 * g + sub;
+            if (qd0 + u < q1 && h < (t == 0 ? p.n_q : p.n_k)) {
+                if (rotated && t < 2) turn<ADJ>(a[u], b[u], cs, sn);
                 uint16_t *dst = nullptr;
-                if (!APPEND || is_q) {
-                    const View &o = is_q ? p.q_out : p.k_out;
+                if (!APPEND || t == 0) {
+                    const View &o = t == 0 ? p.q_out : p.k_out;
                     dst = o.data + outer * o.outer + row * o.row + g * o.group + sub * 128;
                 } else if (page >= 0) {
-                    dst = (is_k ? p.K : p.V) +
+                    dst = (t == 1 ? p.K : p.V) +
                           (((((long long)outer * p.n_pages + page) * p.n_k + h) << p.page_shift) + at) * 128;
                 }
                 if (dst != nullptr) {
