@@ -333,7 +333,8 @@ kvpack_status kvpack_decompress(const kvpack_dims *dims, int32_t n_layers,
  * kvpack_rope -- rotates n_q heads of q and n_k heads of k (either count may be 0, its
  * pointers are then not read) in n_outer x n_rows rows; pos [n_axes][n_outer][n_rows].
  * inverse != 0 turns back (by -t), which is also the gradient of the rotation.  An output
- * may be its input (same data and strides); otherwise outputs overlap nothing.
+ * may be its input (same data and strides); otherwise outputs overlap nothing, themselves
+ * included (a stride of 0 over several rows is refused).
  * n_rows = 0 launches nothing.
  */
 #define KVPACK_MAX_AXES 4

@@ -223,6 +223,11 @@ __device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *tm, int c0,
 
 // ------------------------------------------------------------- warp helpers
 
+// Quotient of non-negative numbers; the 32-bit division is several times faster, and enough for nearly all.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Transpose of an 8x8 b16 matrix held one row pair per lane (mma fragment order).
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     uint32_t y;

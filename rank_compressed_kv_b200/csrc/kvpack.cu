@@ -1098,13 +1098,15 @@ kvpack_status check_heads(const kvpack_heads *v) {
     return KVPACK_OK;
 }
 
-// An output is its input (rotation in place) only with the same strides.
-kvpack_status check_pair(const kvpack_heads *in, const kvpack_heads *out) {
+// An output is its input (rotation in place) only with the same strides, and its rows do not share memory.
+kvpack_status check_pair(const kvpack_heads *in, const kvpack_heads *out, int32_t outer, int32_t rows, int32_t n) {
     kvpack_status s = check_heads(in);
     if (s == KVPACK_OK) s = check_heads(out);
     if (s != KVPACK_OK) return s;
     if (in->data == out->data && (in->outer_stride != out->outer_stride || in->row_stride != out->row_stride ||
                                   in->group_stride != out->group_stride))
+        return KVPACK_ERR_INVALID_ARG;
+    if ((outer > 1 && out->outer_stride == 0) || (rows > 1 && out->row_stride == 0) || (n > 4 && out->group_stride == 0))
         return KVPACK_ERR_INVALID_ARG;
     return KVPACK_OK;
 }
@@ -1155,7 +1157,7 @@ extern "C" {
 kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, const int32_t *pos, int32_t n_outer,
                           int32_t n_rows, int32_t n_q, const kvpack_heads *q, const kvpack_heads *q_out, int32_t n_k,
                           const kvpack_heads *k, const kvpack_heads *k_out, int32_t inverse, void *stream) {
-    if (spec == nullptr || n_outer <= 0 || n_rows < 0 || n_q < 0 || n_k < 0 || n_q + n_k <= 0)
+    if (spec == nullptr || n_outer <= 0 || n_rows < 0 || n_q < 0 || n_k < 0 || (n_q == 0 && n_k == 0))
         return KVPACK_ERR_INVALID_ARG;
     kvpack_status s = check_spec(spec);
     if (s != KVPACK_OK) return s;
@@ -1163,8 +1165,8 @@ kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, cons
     if (n_rows == 0) return KVPACK_OK;
     if (!freq || !pos) return KVPACK_ERR_INVALID_ARG;
     if (!aligned16(freq) || !aligned16(pos)) return KVPACK_ERR_ALIGNMENT;
-    if (n_q > 0 && (s = check_pair(q, q_out)) != KVPACK_OK) return s;
-    if (n_k > 0 && (s = check_pair(k, k_out)) != KVPACK_OK) return s;
+    if (n_q > 0 && (s = check_pair(q, q_out, n_outer, n_rows, n_q)) != KVPACK_OK) return s;
+    if (n_k > 0 && (s = check_pair(k, k_out, n_outer, n_rows, n_k)) != KVPACK_OK) return s;
     rp::Params p{};
     if (n_q > 0) { p.q = view(q); p.q_out = view(q_out); }
     if (n_k > 0) { p.k = view(k); p.k_out = view(k_out); }
@@ -1190,7 +1192,7 @@ kvpack_status kvpack_paged_append(const kvpack_paged_dims *d, int32_t n_layers, 
     if (spec != nullptr && (!freq || !pos)) return KVPACK_ERR_INVALID_ARG;
     if ((q == nullptr) != (q_out == nullptr)) return KVPACK_ERR_INVALID_ARG;
     if ((s = check_heads(k)) != KVPACK_OK || (s = check_heads(v)) != KVPACK_OK) return s;
-    if (q != nullptr && (s = check_pair(q, q_out)) != KVPACK_OK) return s;
+    if (q != nullptr && (s = check_pair(q, q_out, n_layers, n_rows, d->n_q_heads)) != KVPACK_OK) return s;
     if ((s = check_paged_pointers(K_pages, V_pages, block_table, seq_lens)) != KVPACK_OK) return s;
     const void *ptrs[] = {freq, pos, row_offsets};
     for (const void *ptr : ptrs)

@@ -234,11 +234,6 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
     }
 }
 
-// 64-bit quotient; the 32-bit division is several times faster, and enough for nearly all
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 // The places, `total` of them, in runs: the first W0 share `cut` places, the other W1 the rest, each evenly
 // (the first `more` of a share have one place more).  The second share's runs are the shorter ones: they
 // go to the SMs that have finished runs of the first.

@@ -55,6 +55,8 @@ WIDE = [2, 1000]      # spare columns of the table: the attention takes another 
     (1, [4999], 32, 8, 64),
     (1, [40001, 3, 1025], 16, 2, 256),
     (1, [(37 * i) % 211 for i in range(130)], 24, 4, 16),
+    (1, [0] * 40 + [(11 * i) % 37 for i in range(1100)] + [900, 0, 16], 4, 2, 16),
+    (1, [0, 7, 20000, 0], 8, 2, 64),
     (2, [33] * 64, 8, 8, 32),
 ])
 def test_attend_matches_fp64(layers, lens, n_q, n_kv, page, wide):

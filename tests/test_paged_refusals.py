@@ -56,6 +56,10 @@ def test_rope_refusals(kv):
     assert _rope(kv, q=_heads(kv, P + 2)) == 2
     assert _rope(kv, q=_heads(kv, P, (0, 4097, 512))) == 2
     assert _rope(kv, q=_heads(kv), q_out=_heads(kv, P, (0, 8192, 512))) == 1   # in place with other strides
+    assert _rope(kv, q_out=_heads(kv, 2 * P, (0, 0, 512))) == 1    # rows of an output share memory
+    assert _rope(kv, outer=2, q_out=_heads(kv, 2 * P, (0, 4096, 512))) == 1
+    assert _rope(kv, n_q=5, q_out=_heads(kv, 2 * P, (0, 4096, 0))) == 1
+    assert _rope(kv, n_q=2 ** 31 - 1, n_k=2 ** 31 - 1) == 3
     assert _rope(kv, rows=0, freq=None) == 0                       # nothing to do
 
 
