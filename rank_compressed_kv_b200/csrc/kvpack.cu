@@ -162,6 +162,7 @@ bool rs_attrs() {
 bool paged_attrs() {
     namespace pg = kvpack::paged;
     return cudaFuncSetAttribute(pg::attend_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
+           cudaFuncSetAttribute(pg::short_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
            cudaFuncSetAttribute(pg::unit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 pg::kWarps * pg::kRingBytes) == cudaSuccess;
 }
@@ -417,7 +418,8 @@ inline int log2_exact(int x) {
 
 struct PagedPlan {
     long long units;
-    int per_kv, slots, grid, cluster;   // cluster: blocks per unit, 0 where the runs cross units
+    int per_kv, slots, grid;
+    int cluster, shorts;         // blocks per unit, or blocks that take whole units; both 0 where runs cross units
     size_t off_stat, off_acc, total;
 };
 
@@ -425,7 +427,8 @@ struct PagedPlan {
 // long sequence in a batch of short ones would keep its cluster busy alone.  Both forms measured, bf16,
 // 32 query and 8 cached heads, us (unit, runs): 1 x 1024 tokens 5.3 6.9, 16 x 1024 12.6 16.5, 32 x 1024
 // 28.7 30.7, 64 x 512 28.3 31.1; longest of a ragged batch: 16 x 2048 17.7 17.9, 32 x 4096 51.5 53.3.
-constexpr int kUnitTiles = 16;
+constexpr int kUnitTiles = 32;
+constexpr int kShortTiles = 16;  // most tiles of a unit that one warp takes
 
 // Runs for a full B200, fewer where the tables' capacity cannot fill them.
 PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
@@ -437,11 +440,13 @@ PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     pl.slots = (int)(runs < kPlanSMs * pg::kSlotsPerSM ? runs : kPlanSMs * pg::kSlotsPerSM);
     pl.grid = pl.slots * (1 + pg::kSecond);
     const long long wave = kPlanSMs * pg::kUnitBlocksPerSM, cap = (long long)d->max_pages * d->page_size / pg::kTile;
-    int S = pl.units * 8 <= wave ? 8 : pl.units * 4 <= wave ? 4 : pl.units <= wave ? 2 : 1;
-    while (S > 1 && cap * 2 <= (long long)S * pg::kWarps) S >>= 1;       // two warps a tile are too many
+    int S = 8;
+    while (S > 1 && (pl.units * S > wave || cap * 2 <= (long long)S * pg::kWarps)) S >>= 1;   // one wave; two warps a tile are too many
+    const long long warps = kPlanSMs * pg::kSlotsPerSM;
+    if (pl.units > wave && cap <= (pl.units >= warps ? kShortTiles : 4)) pl.shorts = (int)(pl.units < warps ? pl.units : warps);
     // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 33.7, 28.9)
-    if (pl.units <= 2 * wave && cap <= (long long)S * pg::kWarps * kUnitTiles) pl.cluster = S;
-    const size_t slots = pl.cluster > 0 ? 0 : 2 * (size_t)pl.grid;
+    else if (pl.units <= 2 * wave && cap <= (long long)S * pg::kWarps * kUnitTiles) pl.cluster = S;
+    const size_t slots = pl.cluster > 0 || pl.shorts > 0 ? 0 : 2 * (size_t)pl.grid;
     size_t off = 0;
     pl.off_stat = off;
     off = align256(off + slots * 8 * 2 * sizeof(float));
@@ -484,6 +489,9 @@ kvpack_status launch_paged_attend(const kvpack_paged_dims *d, int32_t n_layers, 
     p.slots = pl.slots;
     p.scale2 = softmax_scale * 1.4426950408889634f;
     if (pl.cluster > 0) return launch_unit(p, pl, st) == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
+    if (pl.shorts > 0)
+        return launch_pdl(pg::short_kernel, pl.shorts, 32, pg::kRingBytes, st, p, (int)pl.units) == cudaSuccess
+                   ? KVPACK_OK : KVPACK_ERR_CUDA;
     if (launch_pdl(pg::attend_kernel, pl.grid, 32, pg::kRingBytes, st, p) != cudaSuccess)
         return KVPACK_ERR_CUDA;
     const long long rows = pl.units * pl.per_kv;

@@ -87,6 +87,31 @@ struct State {
     }
 };
 
+// The rows of a unit that one warp has walked from end to end
+__device__ __forceinline__ void finish_unit(const Params &p, long long row, const State &st, int g, int tig) {
+    #pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int hh = 2 * tig + e;
+        if (hh >= p.per_kv) continue;
+        if (p.tpart != nullptr) {
+            float *dst = p.tpart + (row + hh) * decode::kTxtPart;
+            if (g == 0) *reinterpret_cast<float2 *>(dst) = make_float2(st.m[e], st.l[e]);
+            st.store(e, g, dst + 2);
+        } else if (p.lse != nullptr && g == 0) {
+            p.lse[row + hh] = (st.m[e] + log2f(st.l[e])) * kLn2;
+        }
+    }
+    if (p.tpart != nullptr) return;
+    // transposed: lane 4 g + t has entries 8 c + 2 t, + 1 of head g
+    const float i0 = 1.f / st.l[0], i1 = 1.f / st.l[1];
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row + g) * 128) + tig;
+    #pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        const uint32_t v = movmatrix_t(pack_bf16(st.o[c >> 1][2 * (c & 1)] * i0, st.o[c >> 1][2 * (c & 1) + 1] * i1));
+        if (g < p.per_kv) dst[4 * c] = v;
+    }
+}
+
 // A warp's ring of tiles in shared memory: 16 rows of K, then 16 of V, 256 bytes each, 16-byte chunk
 // c of row r at c ^ (r & 7), so that eight rows of one chunk lie in different banks.
 constexpr int kTileBytes = 2 * kTile * 256;
@@ -134,46 +159,60 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
         return n;
     };
 
-    Cursor cu = ld;                                      // the tile being computed; ld runs kSlots - 1 ahead
+    // Cursors: cu is the tile being computed, ld the one to fetch (kSlots - 1 ahead), nx the one after, whose
+    // page number is on its way while ld is fetched.  A unit's queries are loaded with its first tile.
+    Cursor cu = ld, nx = ld;
     int n[kSlots], ahead = 0;                            // tiles' valid rows; tiles fetched and not computed yet
-    int page_ld = page_of(ld);
-    bool more = true;                                    // ld is a tile of the walk
-    auto fetch_next = [&](int &nn, int slot) {
+    uint32_t qn[kSlots][8][2];
+    int page_ld = page_of(ld), page_nx = 0;
+    bool more = true, more_nx = advance(nx), begins = true;          // ld, nx are tiles of the walk; ld begins a unit
+    if (more_nx) page_nx = page_of(nx);
+    auto fetch_next = [&](int &nn, uint32_t (&qs)[8][2], int slot) {
         if (more) {
             nn = fetch(ld, page_ld, slot);
+            if (begins) {
+                const int layer = ld.lk / p.n_kv, kvh = ld.lk - layer * p.n_kv;
+                const long long row = (((long long)layer * p.batch + ld.b) * p.n_kv + kvh) * p.per_kv;
+                const bool ok = g < p.per_kv;
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (row + (ok ? g : 0)) * 128) + tig;
+                #pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    qs[k][0] = ok ? __ldg(src + 8 * k) : 0u;
+                    qs[k][1] = ok ? __ldg(src + 8 * k + 4) : 0u;
+                }
+            }
             ++ahead;
-            more = advance(ld);
-            if (more) page_ld = page_of(ld);
+            begins = ld.t + 1 == ld.nt;
+            more = more_nx;
+            ld = nx;
+            page_ld = page_nx;
+            if (more) {
+                more_nx = advance(nx);
+                if (more_nx) page_nx = page_of(nx);
+            }
         }
         copy_commit();
     };
     #pragma unroll
     for (int i = 0; i < kSlots; ++i) n[i] = 0;
     #pragma unroll
-    for (int i = 0; i < kSlots - 1; ++i) fetch_next(n[i], i);
+    for (int i = 0; i < kSlots - 1; ++i) fetch_next(n[i], qn[i], i);
     const int kx = (lane >> 4) ^ (lane & 7), vx = ((lane >> 3) & 1) ^ (lane & 7);
     const uint32_t krow = (lane & 15) * 256, vrow = 4096 + ((lane & 7) + ((lane >> 4) << 3)) * 256;
     State st;
     st.clear();
     uint32_t qf[8][2];
-    bool fresh = true;                                   // q of cu's unit not loaded yet
+    bool fresh = true;                                   // cu is its unit's first tile of the walk
 
-    auto step = [&](int slot, int &nt, int &nn) {
+    auto step = [&](int slot, int &nt, const uint32_t (&qs)[8][2], int &nn, uint32_t (&qq)[8][2]) {
         copy_wait<kSlots - 2>();                         // the tile has landed
         __syncwarp();                                    // for every lane, and all are done with the one before
-        fetch_next(nn, (slot + kSlots - 1) % kSlots);
         if (fresh) {
-            const int layer = cu.lk / p.n_kv, kvh = cu.lk - layer * p.n_kv;
-            const long long row = (((long long)layer * p.batch + cu.b) * p.n_kv + kvh) * p.per_kv;
-            const bool ok = g < p.per_kv;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (row + (ok ? g : 0)) * 128) + tig;
             #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                qf[k][0] = ok ? __ldg(src + 8 * k) : 0u;
-                qf[k][1] = ok ? __ldg(src + 8 * k + 4) : 0u;
-            }
+            for (int k = 0; k < 8; ++k) { qf[k][0] = qs[k][0]; qf[k][1] = qs[k][1]; }
             fresh = false;
         }
+        fetch_next(nn, qq, (slot + kSlots - 1) % kSlots);
         const uint32_t tb = sb + slot * kTileBytes;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         #pragma unroll
@@ -230,7 +269,7 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
     while (ahead > 0) {
         #pragma unroll
         for (int i = 0; i < kSlots; ++i)
-            if (ahead > 0) step(i, n[i], n[(i + kSlots - 1) % kSlots]);
+            if (ahead > 0) step(i, n[i], qn[i], n[(i + kSlots - 1) % kSlots], qn[(i + kSlots - 1) % kSlots]);
     }
 }
 
@@ -380,27 +419,16 @@ __global__ void __launch_bounds__(32) attend_kernel(const __grid_constant__ Para
         const int layer = cu.lk / p.n_kv, kvh = cu.lk - layer * p.n_kv;
         const long long unit = ((long long)layer * p.batch + cu.b) * p.n_kv + kvh, row = unit * p.per_kv;
         const bool whole = ends && !head;
-        #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int hh = 2 * tig + e;
-            if (hh >= p.per_kv) continue;
-            if (whole && p.tpart == nullptr) {
-                if (p.lse != nullptr && g == 0) p.lse[row + hh] = (st.m[e] + log2f(st.l[e])) * kLn2;
-            } else {
-                const long long slot = 2 * w + (head ? 0 : 1);
-                float *ml = whole ? p.tpart + (row + hh) * decode::kTxtPart : p.stat + (slot * 8 + hh) * 2;
-                if (g == 0) *reinterpret_cast<float2 *>(ml) = make_float2(st.m[e], st.l[e]);
-                st.store(e, g, whole ? ml + 2 : p.acc + (slot * p.per_kv + hh) * 128);
-            }
-        }
-        if (whole && p.tpart == nullptr) {
-            // transposed: lane 4 g + t has entries 8 c + 2 t, + 1 of head g
-            const float i0 = 1.f / st.l[0], i1 = 1.f / st.l[1];
-            uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row + g) * 128) + tig;
+        if (whole) {
+            finish_unit(p, row, st, g, tig);
+        } else {
+            const long long slot = 2 * w + (head ? 0 : 1);
             #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t v = movmatrix_t(pack_bf16(st.o[c >> 1][2 * (c & 1)] * i0, st.o[c >> 1][2 * (c & 1) + 1] * i1));
-                if (g < p.per_kv) dst[4 * c] = v;
+            for (int e = 0; e < 2; ++e) {
+                const int hh = 2 * tig + e;
+                if (hh >= p.per_kv) continue;
+                if (g == 0) *reinterpret_cast<float2 *>(p.stat + (slot * 8 + hh) * 2) = make_float2(st.m[e], st.l[e]);
+                st.store(e, g, p.acc + (slot * p.per_kv + hh) * 128);
             }
         }
         head = false;
@@ -420,6 +448,45 @@ __device__ __forceinline__ void write_row(const Params &p, long long row, bool n
     *reinterpret_cast<uint2 *>(p.out + row * 128 + 4 * lane) =
         make_uint2(pack_bf16(v.x * il, v.y * il), pack_bf16(v.z * il, v.w * il));
     if (p.lse != nullptr && lane == 0) p.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// Many units of few tokens: a warp takes whole units, every gridDim.x-th, its copies running from one into the
+// next.  Nothing to scan and nothing to join.
+__global__ void __launch_bounds__(32) short_kernel(const __grid_constant__ Params p, int units) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    griddep_launch_dependents();
+    const int lane = threadIdx.x, g = lane >> 2, tig = lane & 3;
+    // unit u as a cursor's sequence, head and length; x = u
+    auto enter = [&](Cursor &c, int u) {
+        const int lb = u / p.n_kv, layer = lb / p.batch;
+        c.x = u;
+        c.b = lb - layer * p.batch;
+        c.lk = layer * p.n_kv + u - lb * p.n_kv;
+        c.t = 0;
+        c.len = clamped_len(p, c.b, c.lk == 0);
+        c.nt = (c.len + kTile - 1) / kTile;
+    };
+    // the first unit from u on that has tokens
+    auto seek = [&](Cursor &c, int u) {
+        for (; u < units; u += gridDim.x) {
+            enter(c, u);
+            if (c.len > 0) return true;
+        }
+        return false;
+    };
+    griddep_wait();
+    Cursor first{};
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {             // rows of sequences without tokens
+        enter(first, u);
+        if (first.len == 0)
+            for (int h = 0; h < p.per_kv; ++h)
+                write_row(p, (long long)u * p.per_kv + h, true, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), lane);
+    }
+    if (!seek(first, blockIdx.x)) return;
+    auto advance = [&](Cursor &c) { return ++c.t < c.nt || seek(c, (int)c.x + (int)gridDim.x); };
+    walk(p, smem, first, advance, [&](const Cursor &cu, bool, const State &st) {
+        finish_unit(p, cu.x * p.per_kv, st, g, tig);
+    });
 }
 
 // The parts of the units that several runs share, in their order,
