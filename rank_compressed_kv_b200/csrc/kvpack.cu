@@ -418,17 +418,21 @@ inline int log2_exact(int x) {
 
 struct PagedPlan {
     long long units;
-    int per_kv, slots, grid;
+    int per_kv, slots;
     int cluster, shorts;         // blocks per unit, or blocks that take whole units; both 0 where runs cross units
     size_t off_stat, off_acc, total;
 };
 
-// A cluster per unit where the tables' capacity gives a warp at most this many tiles: with more, one
-// long sequence in a batch of short ones would keep its cluster busy alone.  Both forms measured, bf16,
-// 32 query and 8 cached heads, us (unit, runs): 1 x 1024 tokens 5.3 6.9, 16 x 1024 12.6 16.5, 32 x 1024
-// 28.7 30.7, 64 x 512 28.3 31.1; longest of a ragged batch: 16 x 2048 17.7 17.9, 32 x 4096 51.5 53.3.
+// Three forms, by the number of units and the tables' capacity (the lengths are on the device).  Measured, bf16, us:
+//   a cluster of blocks per unit, one wave of blocks      few units, caches of up to kUnitTiles tiles a warp
+//     1 x 1024 tokens (8 units) 5.3, runs 7.0; 32 x 1024 (256 units) 24.7, 30.6; ragged up to 2048: 31.9, 32.2
+//   a warp per unit                                       enough units for every warp, up to kShortTiles tiles
+//     1024 units of 16 tokens 4.3, runs 13; of 512 45, 59; of 1024 85, 99; ragged up to 1024: 65, 62
+//     also few tiles on units past one wave of clusters: 512 units of 64 tokens 6.9, 11.5
+//   even runs over all units, joined                      the rest: one long sequence keeps every warp busy
+// The limits keep a long sequence among short ones, which only the runs share out, to some tens of us.
 constexpr int kUnitTiles = 32;
-constexpr int kShortTiles = 16;  // most tiles of a unit that one warp takes
+constexpr int kShortTiles = 64;
 
 // Runs for a full B200, fewer where the tables' capacity cannot fill them.
 PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
@@ -438,15 +442,15 @@ PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     const long long places = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile + 1);
     const long long runs = (places + pg::kMinPlaces - 1) / pg::kMinPlaces;
     pl.slots = (int)(runs < kPlanSMs * pg::kSlotsPerSM ? runs : kPlanSMs * pg::kSlotsPerSM);
-    pl.grid = pl.slots * (1 + pg::kSecond);
     const long long wave = kPlanSMs * pg::kUnitBlocksPerSM, cap = (long long)d->max_pages * d->page_size / pg::kTile;
     int S = 8;
     while (S > 1 && (pl.units * S > wave || cap * 2 <= (long long)S * pg::kWarps)) S >>= 1;   // one wave; two warps a tile are too many
     const long long warps = kPlanSMs * pg::kSlotsPerSM;
-    if (pl.units > wave && cap <= (pl.units >= warps ? kShortTiles : 4)) pl.shorts = (int)(pl.units < warps ? pl.units : warps);
+    if (pl.units > wave && cap <= (pl.units * 20 >= warps * 17 ? kShortTiles : 4))
+        pl.shorts = (int)(pl.units < warps ? pl.units : warps);
     // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 33.7, 28.9)
     else if (pl.units <= 2 * wave && cap <= (long long)S * pg::kWarps * kUnitTiles) pl.cluster = S;
-    const size_t slots = pl.cluster > 0 || pl.shorts > 0 ? 0 : 2 * (size_t)pl.grid;
+    const size_t slots = pl.cluster > 0 || pl.shorts > 0 ? 0 : 2 * (size_t)pl.slots;
     size_t off = 0;
     pl.off_stat = off;
     off = align256(off + slots * 8 * 2 * sizeof(float));
@@ -492,7 +496,7 @@ kvpack_status launch_paged_attend(const kvpack_paged_dims *d, int32_t n_layers, 
     if (pl.shorts > 0)
         return launch_pdl(pg::short_kernel, pl.shorts, 32, pg::kRingBytes, st, p, (int)pl.units) == cudaSuccess
                    ? KVPACK_OK : KVPACK_ERR_CUDA;
-    if (launch_pdl(pg::attend_kernel, pl.grid, 32, pg::kRingBytes, st, p) != cudaSuccess)
+    if (launch_pdl(pg::attend_kernel, pl.slots, 32, pg::kRingBytes, st, p) != cudaSuccess)
         return KVPACK_ERR_CUDA;
     const long long rows = pl.units * pl.per_kv;
     // warps per row: so many that each has about four parts

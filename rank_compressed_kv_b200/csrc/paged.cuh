@@ -20,8 +20,7 @@ namespace paged {
 constexpr int kTile = 16;
 constexpr int kWarps = 4;           // of unit_kernel's blocks
 constexpr int kThreads = kWarps * 32;
-constexpr int kSlotsPerSM = 8;      // runs of the first share per SM
-constexpr int kTwoShares = 64, kCut = 12, kSecond = 1;
+constexpr int kSlotsPerSM = 8;      // runs, and so warps, per SM
 constexpr int kUnitBlocksPerSM = 2; // of unit_kernel
 constexpr int kSlots = 3;           // tiles of a warp in shared memory
 constexpr int kMinPlaces = 2;       // shortest run
@@ -36,7 +35,7 @@ struct Params {
     float *tpart;                   // [layers * batch][n_q][kTxtPart]: (m, l, sum p V) of each head, or null
     float *stat;                    // [2 * runs][8][2]: m, l of a run's part; slot 2 w for the unit that an
     float *acc;                     // [2 * runs][per_kv][128]     earlier run began, 2 w + 1 for the one it leaves
-    int layers, batch, n_kv, per_kv, n_pages, max_pages, page_shift, slots;   // slots: runs of the first share, at most
+    int layers, batch, n_kv, per_kv, n_pages, max_pages, page_shift, slots;   // slots: runs at most
     float scale2;
 };
 
@@ -214,18 +213,19 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
         }
         fetch_next(nn, qq, (slot + kSlots - 1) % kSlots);
         const uint32_t tb = sb + slot * kTileBytes;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        // two sums of four products each: half the chain of dependent instructions, which bounds a lone warp
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
         #pragma unroll
         for (int k = 0; k < 8; ++k) {
             uint32_t a[4];
             ldsm_x4(tb + krow + (((2 * k) ^ kx) << 4), a[0], a[1], a[2], a[3]);
-            mma_bf16(s, a, qf[k][0], qf[k][1]);
+            mma_bf16(k & 1 ? s2 : s, a, qf[k][0], qf[k][1]);
         }
         // s[0], s[1]: token g, heads 2 tig, 2 tig + 1; s[2], s[3]: token g + 8
-        s[0] = g < nt ? s[0] * p.scale2 : -INFINITY;
-        s[1] = g < nt ? s[1] * p.scale2 : -INFINITY;
-        s[2] = g + 8 < nt ? s[2] * p.scale2 : -INFINITY;
-        s[3] = g + 8 < nt ? s[3] * p.scale2 : -INFINITY;
+        s[0] = g < nt ? (s[0] + s2[0]) * p.scale2 : -INFINITY;
+        s[1] = g < nt ? (s[1] + s2[1]) * p.scale2 : -INFINITY;
+        s[2] = g + 8 < nt ? (s[2] + s2[2]) * p.scale2 : -INFINITY;
+        s[3] = g + 8 < nt ? (s[3] + s2[3]) * p.scale2 : -INFINITY;
         float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
         #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
@@ -273,33 +273,20 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
     }
 }
 
-// The places, `total` of them, in runs: the first W0 share `cut` places, the other W1 the rest, each evenly
-// (the first `more` of a share have one place more).  The second share's runs are the shorter ones: they
-// go to the SMs that have finished runs of the first.
+// The places, `total` of them, in W even runs: the first `more` have base + 1 places, the others base.
 struct Runs {
-    long long W0, W, cut, base0, more0, base1, more1;
+    long long W, base, more;
 
     __device__ __forceinline__ Runs(long long total, int slots) {
         const long long most = total / kMinPlaces;
-        W0 = most < 1 ? 1 : most < slots ? most : slots;
-        const bool two = total >= W0 * kTwoShares;
-        const long long W1 = two ? W0 * kSecond : 0;
-        cut = two ? total * kCut / 16 : total;
-        W = W0 + W1;
-        base0 = quotient(cut, W0);
-        more0 = cut - base0 * W0;
-        base1 = two ? quotient(total - cut, W1) : 0;
-        more1 = total - cut - base1 * W1;
+        W = most < 1 ? 1 : most < slots ? most : slots;
+        base = quotient(total, W);
+        more = total - base * W;
     }
-    __device__ __forceinline__ long long first(long long w) const {
-        if (w <= W0) return w * base0 + (w < more0 ? w : more0);
-        w -= W0;
-        return cut + w * base1 + (w < more1 ? w : more1);
-    }
+    __device__ __forceinline__ long long first(long long w) const { return w * base + (w < more ? w : more); }
     __device__ __forceinline__ long long of(long long x) const {
-        const long long base = x < cut ? base0 : base1, more = x < cut ? more0 : more1;
-        const long long y = x < cut ? x : x - cut, w = x < cut ? 0 : W0, longer = more * (base + 1);
-        return w + (y < longer ? quotient(y, base + 1) : more + quotient(y - longer, base));
+        const long long longer = more * (base + 1);
+        return x < longer ? quotient(x, base + 1) : more + quotient(x - longer, base);
     }
 };
 
@@ -367,9 +354,9 @@ struct Lengths {
     }
 };
 
-// A block is one warp and takes one run.  The runs of the first share fill the GPU; those of the
-// second go where an SM is done, since SMs do not get equal parts of the memory's bandwidth (with equal
-// shares for all, the last warp ended 15 % after the median).
+// A block is one warp and takes one run; the runs fill the GPU once.  SMs do not get equal parts of the
+// memory's bandwidth, so the last warp ends 10 to 15 % after the median; shorter runs that go where an SM is
+// done even that out, but each end of a run costs about a tile and they gain nothing.
 __global__ void __launch_bounds__(32) attend_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) unsigned char smem[];
     // in this order: the join may then read the lengths, which a kernel before this one may write
