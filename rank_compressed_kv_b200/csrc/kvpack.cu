@@ -1142,22 +1142,27 @@ cudaError_t launch_rope_u(const rp::Params &p, long long grid, bool adjacent, cu
                     : launch_pdl(rp::rope_kernel<APPEND, false, U>, (int)grid, rp::kThreads, 0, st, p);
 }
 
-// Few rows: a row's quads split over as many warps as the GPU holds, two loaded at a time (576 rows of 64
-// heads 4.0 us; 4.2 with three, 4.7 with four).  Many rows: a warp each, and more on the way: four quads
-// in the rotation (100352 rows of 32 heads 247 us; 258 with three, 263 with two), three in the append,
-// whose stores scatter (53 k rows of 36 heads 151 us; 155 with two, 162 with four), less for few heads.
+// A row's quads of heads are split over warps while the rows leave warps of the GPU free: one each where all
+// fit at once, else shares of two and more, up to two waves (2500 rows of 64 heads 16.6 us; 21.3 with a warp
+// per row).  Quads on the way at a time: four in the rotation of many rows (100352 rows of 32 heads 247 us;
+// 258 with three, 263 with two), three in the append, whose stores scatter (53 k rows of 36 heads 151 us; 155
+// with two, 162 with four), fewer where a warp has few.
 template <bool APPEND>
 kvpack_status launch_rope(rp::Params &p, long long orows, bool adjacent, cudaStream_t st) {
-    const long long splits = (long long)kPlanSMs * rp::kWarpsPerSM / orows;
-    p.splits = (int)(splits < 1 ? 1 : splits > p.quads ? p.quads : splits);
-    p.qpw = (p.quads + p.splits - 1) / p.splits;
+    const long long warps = (long long)kPlanSMs * rp::kWarpsPerSM;
+    long long splits = 2 * warps / orows;
+    if (orows * p.quads <= warps) splits = p.quads;
+    else if (splits > p.quads / 2) splits = p.quads / 2;
+    if (splits < 1) splits = 1;
+    p.qpw = (int)((p.quads + splits - 1) / splits);
     p.splits = (p.quads + p.qpw - 1) / p.qpw;
     p.items = orows * p.splits;
     const long long grid = (p.items + rp::kThreads / 32 - 1) / (rp::kThreads / 32);
     if (grid > 0x7fffffffLL) return KVPACK_ERR_UNSUPPORTED;
+    const int most = APPEND ? (p.splits > 1 ? 2 : 3) : (p.splits > 1 ? 3 : 4);
     cudaError_t e;
-    if (p.splits > 1 || (APPEND && p.quads < 6)) e = launch_rope_u<APPEND, 2>(p, grid, adjacent, st);
-    else if (APPEND || p.quads < 4) e = launch_rope_u<APPEND, 3>(p, grid, adjacent, st);
+    if (most == 2 || p.qpw < 3 || (APPEND && p.quads < 6)) e = launch_rope_u<APPEND, 2>(p, grid, adjacent, st);
+    else if (most == 3 || p.qpw < 4) e = launch_rope_u<APPEND, 3>(p, grid, adjacent, st);
     else e = launch_rope_u<APPEND, APPEND ? 3 : 4>(p, grid, adjacent, st);
     return e == cudaSuccess ? KVPACK_OK : KVPACK_ERR_CUDA;
 }
