@@ -37,8 +37,9 @@ struct Params {
     int batch, n_pages, max_pages, page_shift;
 };
 
-// The slot a row's key and value go to: (page, offset in it), page < 0 for none.  found: the row
-// belongs to a sequence (rows behind the last one, and idle sequences of length 0, do not).
+// The slot a row's key and value go to: (page, offset in it), the page's number unchecked, < 0 for an index
+// out of range.  found: the row belongs to a sequence (rows behind the last one, and idle sequences of
+// length 0, do not).
 __device__ __forceinline__ void find_slot(const Params &p, int row, int lane, bool &found, int &page, int &at) {
     found = false;
     page = -1;
@@ -71,11 +72,6 @@ __device__ __forceinline__ void find_slot(const Params &p, int row, int lane, bo
     found = true;
     const long long cap = (long long)p.max_pages << p.page_shift;
     if (index >= 0 && index < cap) page = __ldg(p.table + (long long)seq * p.max_pages + (index >> p.page_shift));
-    if (page < 0 || page >= p.n_pages) {
-        page = -1;
-        if (lane == 0) report_error(KVPACK_ERR_PAGE);
-        return;
-    }
     at = index & ((1 << p.page_shift) - 1);
 }
 
@@ -149,6 +145,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     };
     load(q0);                                   // on their way while the angles and the slot are worked out
 
+    const int p0 = 8 * c + 2 * sub;             // the lane's two pairs
+    auto position = [&](int i) {
+        const uint32_t w = p0 < 16 ? p.axis2[0] : p0 < 32 ? p.axis2[1] : p0 < 48 ? p.axis2[2] : p.axis2[3];
+        const int ax = (w >> (2 * ((p0 + i) & 15))) & 3;
+        return __ldg(p.pos + ax * p.pos_axis + outer * p.pos_outer + row);
+    };
+    // before the slot's chain of loads; without one they only cost registers there
+    int early_pos[2] = {0, 0};
+    double early_freq[2] = {0., 0.};
+    if (APPEND && rotated) {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            early_pos[i] = position(i);
+            early_freq[i] = __ldg(p.freq + p0 + i);
+        }
+    }
     bool found = true;
     int page = 0, at = 0;
     if constexpr (APPEND) {
@@ -160,13 +172,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     if (p.rot8 > 0) {
         float c2[2] = {1.f, 1.f}, s2[2] = {0.f, 0.f};
         if (rotated) {
-            const int p0 = 8 * c + 2 * sub;
             #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t w = p0 < 16 ? p.axis2[0] : p0 < 32 ? p.axis2[1] : p0 < 48 ? p.axis2[2] : p.axis2[3];
-                const int ax = (w >> (2 * ((p0 + i) & 15))) & 3;
-                const int at_pos = __ldg(p.pos + ax * p.pos_axis + outer * p.pos_outer + row);
-                const double turns = (double)at_pos * (__ldg(p.freq + p0 + i) * 0.15915494309189535);
+                const int at_pos = APPEND ? early_pos[i] : position(i);
+                const double freq = APPEND ? early_freq[i] : __ldg(p.freq + p0 + i);
+                const double turns = (double)at_pos * (freq * 0.15915494309189535);
                 const float part = (float)(turns - rint(turns));
                 sincospif(2.f * part, &s2[i], &c2[i]);
             }
@@ -178,6 +188,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         }
     }
 
+    if constexpr (APPEND) {
+        if (page < 0 || page >= p.n_pages) {
+            page = -1;
+            if (lane == 0) report_error(KVPACK_ERR_PAGE);
+        }
+    }
     for (int qd0 = q0; qd0 < q1; qd0 += U) {
         if (qd0 > q0) load(qd0);
         #pragma unroll
