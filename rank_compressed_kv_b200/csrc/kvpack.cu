@@ -1144,13 +1144,14 @@ cudaError_t launch_rope_u(const rp::Params &p, long long grid, bool adjacent, cu
 
 // A row's quads of heads are split over warps while the rows leave warps of the GPU free: one each where all
 // fit at once, else shares of two and more, up to two waves (2500 rows of 64 heads 16.6 us; 21.3 with a warp
-// per row).  Quads on the way at a time: four in the rotation of many rows (100352 rows of 32 heads 247 us;
+// per row), or three where a warp per row would half fill the second (6000 rows 34.0 us; 36.1).  Quads on the way at a time: four in the rotation of many rows (100352 rows of 32 heads 247 us;
 // 258 with three, 263 with two), three in the append, whose stores scatter (53 k rows of 36 heads 151 us; 155
 // with two, 162 with four), fewer where a warp has few.
 template <bool APPEND>
 kvpack_status launch_rope(rp::Params &p, long long orows, bool adjacent, cudaStream_t st) {
     const long long warps = (long long)kPlanSMs * rp::kWarpsPerSM;
     long long splits = 2 * warps / orows;
+    if (splits == 1 && orows > warps && 3 * warps >= 2 * orows && p.quads >= 6) splits = 2;
     if (orows * p.quads <= warps) splits = p.quads;
     else if (splits > p.quads / 2) splits = p.quads / 2;
     if (splits < 1) splits = 1;

@@ -39,7 +39,9 @@ def _dev(*ts):
     return [t.to(DEV) for t in ts]
 
 
-WIDE = [2, 1000]      # spare columns of the table: the attention takes another form where it could hold long caches
+# spare columns of the table: where it could hold long caches, the attention takes its runs over all units; else a
+# cluster of blocks per unit, or (some thousand units of up to 1024 tokens) a warp per unit
+WIDE = [2, 2100]
 
 
 @pytest.mark.parametrize("wide", WIDE)
@@ -58,6 +60,9 @@ WIDE = [2, 1000]      # spare columns of the table: the attention takes another 
     (1, [0] * 40 + [(11 * i) % 37 for i in range(1100)] + [900, 0, 16], 4, 2, 16),
     (1, [0, 7, 20000, 0], 8, 2, 64),
     (2, [33] * 64, 8, 8, 32),
+    (1, [(29 * i) % 600 for i in range(260)], 28, 4, 128),
+    (4, [0, 1, 17, 300] * 10, 32, 32, 16),
+    (1, [3000, 5, 0, 16390], 8, 4, 256),
 ])
 def test_attend_matches_fp64(layers, lens, n_q, n_kv, page, wide):
     """Slots that hold no token are NaN, table entries behind the last page out of range."""
@@ -380,10 +385,10 @@ def test_prompts_and_steps_together():
     assert kv.last_device_status() == 0
 
 
-def _paged_tail(c, w, n_layers, lens, page, seed):
+def _paged_tail(c, w, n_layers, lens, page, seed, wide):
     """The dense text tails K_text, V_text [units][L][4][128] of a decode case as pools and a table."""
     g = torch.Generator().manual_seed(seed)
-    table, n_pages = pages_for(lens, page, g)
+    table, n_pages = pages_for(lens, page, g, wide=wide)
     pools = []
     for name in ("K_text", "V_text"):
         dense = torch.from_numpy(c[name].view(np.int16)).view(torch.bfloat16)
@@ -397,16 +402,17 @@ def _paged_tail(c, w, n_layers, lens, page, seed):
     return pools[0], pools[1], table.to(DEV), n_pages
 
 
+@pytest.mark.parametrize("wide", WIDE)
 @pytest.mark.parametrize("batch,layers,n_q,n_kv,T,lens,rank_lo", [
     (2, 2, 8, 8, 300, [45, 45], 16), (3, 1, 32, 8, 700, [0, 1, 130], 16), (2, 1, 28, 4, 1500, [17, 1000], 16),
     (2, 1, 32, 4, 600, [64, 0], 0), (1, 1, 8, 8, 64, [0], 16),
-    (2, 1, 16, 8, 200, [5000, 77], 16)])
-def test_decode_with_a_paged_text_tail_matches_the_oracle(batch, layers, n_q, n_kv, T, lens, rank_lo):
+    (2, 1, 16, 8, 200, [5000, 77], 16), (36, 1, 32, 32, 40, [0, 5, 40] * 12, 16)])
+def test_decode_with_a_paged_text_tail_matches_the_oracle(batch, layers, n_q, n_kv, T, lens, rank_lo, wide):
     import rank_compressed_kv_b200 as kv
     w = synth.Workload("paged", 50 + T, batch, layers, n_q, n_kv, T, max(max(lens), 1), 1, "lowrank32")
     Lcap = w.text0
     c = cases.decode_case(w, n_layers=layers, T=T, Lcap=Lcap)
-    K, V, table, n_pages = _paged_tail(c, w, layers, lens, 32, T)
+    K, V, table, n_pages = _paged_tail(c, w, layers, lens, 32, T, wide)
     dims = kv.Dims(batch=batch, n_q_heads=n_q, n_kv_heads=n_kv, T_vis=T, L_text_cap=0, rank_lo=rank_lo)
     pd = kv.PagedDims(batch, n_q, n_kv, 32, n_pages, table.shape[1])
     g = {k: bf(c[k]) for k in ("q", "CK_lo", "CK_hi", "BK", "CV_lo", "CV_hi", "BV")}
@@ -417,8 +423,9 @@ def test_decode_with_a_paged_text_tail_matches_the_oracle(batch, layers, n_q, n_
                          table, torch.tensor(lens, dtype=torch.int32, device=DEV), u32(c["mask"]), 1.0, out, mass, ws)
     assert kv.last_device_status() == 0
     o, ms = out.float().cpu().numpy(), mass.cpu().numpy()
+    refs = {n: oracle_decode(w, c, n, rank_lo=rank_lo) for n in set(lens)}
     for b, n in enumerate(lens):                      # the oracle has one text length for the batch: row by row
-        ref_o, ref_m = oracle_decode(w, c, n, rank_lo=rank_lo)
+        ref_o, ref_m = refs[n]
         rows = [l * batch + b for l in range(layers)]
         units = [r * w.groups + G for r in rows for G in range(w.groups)]
         got_u = cases.per_unit_outputs(w, o)
