@@ -151,6 +151,10 @@ struct Call {
         }
         if (s1 != 1 || (sh != 128 && n > 1))
             throw Refused(std::string(what) + ": a head's entries and the heads of a row (of four) lie side by side");
+        // strides of dimensions of one are as good as any
+        if (outer == 1) h.outer_stride = 0;
+        if (rows == 1) h.row_stride = 0;
+        if (n <= 4) h.group_stride = 512;
         seen(t, what);
         h.data = static_cast<uint16_t *>(t.data_ptr());
         return h;

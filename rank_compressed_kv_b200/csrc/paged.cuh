@@ -56,7 +56,7 @@ struct Cursor {
 
 __device__ __forceinline__ int clamped_len(const Params &p, int b, bool report) {
     const long long cap = (long long)p.max_pages << p.page_shift;
-    int len = __ldg(p.lens + b);
+    int len = p.lens[b];                                 // a plain load: the kernel may start before its writer ends
     if (len < 0 || len > cap) {
         if (report) report_error(KVPACK_ERR_PAGE);
         len = len < 0 ? 0 : (int)cap;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
     const int page_mask = (1 << p.page_shift) - 1;
     const uint32_t sb = smem_u32(ring);
     auto page_of = [&](const Cursor &c) {
-        return __ldg(p.table + (long long)c.b * p.max_pages + ((c.t * kTile) >> p.page_shift));
+        return p.table[(long long)c.b * p.max_pages + ((c.t * kTile) >> p.page_shift)];
     };
     // copy of lane: row 2 i + lane / 16, chunk lane % 16, i < 8
     const int row2 = lane >> 4, chunk = lane & 15;
@@ -188,8 +188,8 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q + (row + (ok ? g : 0)) * 128) + tig;
                 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    qs[k][0] = ok ? __ldg(src + 8 * k) : 0u;
-                    qs[k][1] = ok ? __ldg(src + 8 * k + 4) : 0u;
+                    qs[k][0] = ok ? src[8 * k] : 0u;
+                    qs[k][1] = ok ? src[8 * k + 4] : 0u;
                 }
             }
             ++ahead;

@@ -20,6 +20,7 @@ struct View {
     long long outer, row, group;
 };
 
+// Inputs are read with plain loads: the kernel may start before the kernel that writes them ends.
 struct Params {
     View q, q_out, k, k_out, v;     // append: k_out is not used, k and v go into the pages
     const int32_t *pos;             // [axes][outers][rows], append: [axes][rows]
@@ -47,7 +48,7 @@ __device__ __forceinline__ void find_slot(const Params &p, int row, int lane, bo
     int seq, index;
     if (p.offsets == nullptr) {
         seq = row;
-        const int len = __ldg(p.lens + row);
+        const int len = p.lens[row];
         if (len == 0) return;
         index = len - 1;
     } else {
@@ -56,7 +57,7 @@ __device__ __forceinline__ void find_slot(const Params &p, int row, int lane, bo
         int last = -1;
         while (lo < hi) {
             const int step = (hi - lo + 31) >> 5, at32 = lo + lane * step;
-            const bool le = at32 < hi && __ldg(p.offsets + at32) <= row;
+            const bool le = at32 < hi && p.offsets[at32] <= row;
             const int cnt = __popc(__ballot_sync(0xffffffffu, le));
             if (cnt == 0) break;
             last = lo + (cnt - 1) * step;
@@ -65,13 +66,13 @@ __device__ __forceinline__ void find_slot(const Params &p, int row, int lane, bo
         }
         if (last < 0 || last >= p.batch) return;
         seq = last;
-        const int o0 = __ldg(p.offsets + seq), o1 = __ldg(p.offsets + seq + 1);
+        const int o1 = p.offsets[seq + 1];
         if (row >= o1) return;
-        index = __ldg(p.lens + seq) - (o1 - row);
+        index = p.lens[seq] - (o1 - row);
     }
     found = true;
     const long long cap = (long long)p.max_pages << p.page_shift;
-    if (index >= 0 && index < cap) page = __ldg(p.table + (long long)seq * p.max_pages + (index >> p.page_shift));
+    if (index >= 0 && index < cap) page = p.table[(long long)seq * p.max_pages + (index >> p.page_shift)];
     at = index & ((1 << p.page_shift) - 1);
 }
 
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     auto position = [&](int i) {
         const uint32_t w = p0 < 16 ? p.axis2[0] : p0 < 32 ? p.axis2[1] : p0 < 48 ? p.axis2[2] : p.axis2[3];
         const int ax = (w >> (2 * ((p0 + i) & 15))) & 3;
-        return __ldg(p.pos + ax * p.pos_axis + outer * p.pos_outer + row);
+        return p.pos[ax * p.pos_axis + outer * p.pos_outer + row];
     };
     // before the slot's chain of loads; without one they only cost registers there
     int early_pos[2] = {0, 0};
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
             early_pos[i] = position(i);
-            early_freq[i] = __ldg(p.freq + p0 + i);
+            early_freq[i] = p.freq[p0 + i];
         }
     }
     bool found = true;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
             #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int at_pos = APPEND ? early_pos[i] : position(i);
-                const double freq = APPEND ? early_freq[i] : __ldg(p.freq + p0 + i);
+                const double freq = APPEND ? early_freq[i] : p.freq[p0 + i];
                 const double turns = (double)at_pos * (freq * 0.15915494309189535);
                 const float part = (float)(turns - rint(turns));
                 sincospif(2.f * part, &s2[i], &c2[i]);

@@ -385,6 +385,58 @@ def test_prompts_and_steps_together():
     assert kv.last_device_status() == 0
 
 
+@pytest.mark.parametrize("wide", WIDE)
+def test_launches_behind_one_another_see_what_came_before(wide):
+    """Steps without a wait between them (kernels start before their predecessors end): inputs, lengths and table written
+    by the kernel just before, append, attention, and an overwrite of the inputs right behind; bit for bit as with waits."""
+    import rank_compressed_kv_b200 as kv
+    n_q, n_kv, page, B = 32, 8, 32, 6
+    g = torch.Generator().manual_seed(5)
+    start = [300, 1, 77, 640, 0, 31]
+    steps = 12
+    table, n_pages = pages_for([n + steps for n in start], page, g, wide=wide)
+    dims = kv.PagedDims(B, n_q, n_kv, page, n_pages, table.shape[1])
+    spec = kv.Rope(n_axes=2)
+    freq = spec.frequencies(1e4)
+    K0, V0 = normal(g, 1, n_pages, n_kv, page, D).to(DEV), normal(g, 1, n_pages, n_kv, page, D).to(DEV)
+    xs = normal(g, steps, B, n_q + 2 * n_kv, D).to(DEV)
+    noise = torch.randn(4096, 4096, device=DEV)
+    ws = torch.empty(kv.paged_decode_workspace(dims, 1), dtype=torch.uint8, device=DEV)
+
+    def play(wait):
+        K, V = K0.clone(), V0.clone()
+        x, q = torch.zeros_like(xs[0]), torch.zeros(B, n_q, D, dtype=torch.bfloat16, device=DEV)
+        lens, td = torch.tensor(start, dtype=torch.int32, device=DEV), torch.full_like(table, -1, device=DEV)
+        real = table.to(DEV)
+        pos = torch.zeros(2, B, dtype=torch.int32, device=DEV)
+        outs = []
+        for i in range(steps):
+            noise @ noise                                  # something to still be running
+            x.copy_(xs[i])
+            td.copy_(real)
+            pos.copy_(lens[None].expand(2, B))
+            lens += 1
+            if wait:
+                torch.cuda.synchronize()
+            kv.paged_append(dims, 1, spec, freq, pos, x[:, :n_q], x[:, n_q:n_q + n_kv], x[:, n_q + n_kv:], None, lens, td, q, K, V)
+            if wait:
+                torch.cuda.synchronize()
+            out, lse = torch.empty_like(q), torch.empty(B, n_q, device=DEV)
+            kv.paged_decode_attn(dims, 1, q, K, V, td, lens, 0.1, out, lse, ws)
+            x.fill_(float("nan"))
+            q.fill_(float("nan"))
+            td.fill_(-1)
+            outs += [out, lse]
+            if wait:
+                torch.cuda.synchronize()
+        return outs + [K, V]
+
+    with_waits, without = play(True), play(False)
+    assert kv.last_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(with_waits, without))
+    assert not any(bool(torch.isnan(t).any()) for t in without)
+
+
 def _paged_tail(c, w, n_layers, lens, page, seed, wide):
     """The dense text tails K_text, V_text [units][L][4][128] of a decode case as pools and a table."""
     g = torch.Generator().manual_seed(seed)

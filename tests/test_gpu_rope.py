@@ -119,6 +119,17 @@ def test_nothing_outside_the_rows_is_written_and_empty_calls_do_nothing():
     kv.rope(spec, freq, torch.empty(1, 0, dtype=torch.int32, device=DEV), x[:0], x[:0])
 
 
+def test_strides_of_single_rows_do_not_matter():
+    kv, spec = _spec(128, 1, False, False)
+    freq = spec.frequencies(1e4, "cpu")
+    x = normal(torch.Generator().manual_seed(1), 1, 1, 3, 128)
+    odd = torch.as_strided(x.to(DEV), (1, 1, 3, 128), (7, 3, 128, 1))
+    out = torch.empty(1, 1, 3, 128, dtype=torch.bfloat16, device=DEV)
+    pos = torch.tensor([[[12]]], dtype=torch.int32)
+    kv.rope(spec, freq.to(DEV), pos.to(DEV), odd, out)
+    _check(kv, spec, freq, pos, x, out.cpu())
+
+
 def test_captured_and_on_another_stream():
     kv, spec = _spec(128, 3, False, False)
     g = torch.Generator().manual_seed(3)
