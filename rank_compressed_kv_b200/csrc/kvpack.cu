@@ -441,11 +441,15 @@ PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     pl.per_kv = d->n_q_heads / d->n_kv_heads;
     const long long places = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile + 1);
     const long long runs = (places + pg::kMinPlaces - 1) / pg::kMinPlaces;
-    pl.slots = (int)(runs < kPlanSMs * pg::kSlotsPerSM ? runs : kPlanSMs * pg::kSlotsPerSM);
+    // as many runs for each of a few units, so that the ends of equal units are ends of runs: 4 x 66560 tokens
+    // (32 units) 166 us with 1024 runs, 174 with 1036 or, eight an SM, 1184
+    long long most = (long long)kPlanSMs * pg::kSlotsPerSM;
+    if (pl.units * 8 <= most) most -= most % pl.units;
+    pl.slots = (int)(runs < most ? runs : most);
     const long long wave = kPlanSMs * pg::kUnitBlocksPerSM, cap = (long long)d->max_pages * d->page_size / pg::kTile;
     int S = 8;
     while (S > 1 && (pl.units * S > wave || cap * 2 <= (long long)S * pg::kWarps)) S >>= 1;   // one wave; two warps a tile are too many
-    const long long warps = kPlanSMs * pg::kSlotsPerSM;
+    const long long warps = kPlanSMs * pg::kShortPerSM;
     if (pl.units > wave && cap <= (pl.units * 20 >= warps * 17 ? kShortTiles : 4))
         pl.shorts = (int)(pl.units < warps ? pl.units : warps);
     // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 33.7, 28.9)

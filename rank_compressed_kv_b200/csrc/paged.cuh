@@ -30,7 +30,8 @@ namespace paged {
 constexpr int kTile = 16;
 constexpr int kWarps = 4;           // of unit_kernel's blocks
 constexpr int kThreads = kWarps * 32;
-constexpr int kSlotsPerSM = 8;      // runs, and so warps, per SM
+constexpr int kSlotsPerSM = 7;      // runs, and so warps, per SM: one less than it holds
+constexpr int kShortPerSM = 8;      // warps of short_kernel per SM
 constexpr int kUnitBlocksPerSM = 2; // of unit_kernel
 constexpr int kSlots = 3;           // tiles of a warp in shared memory
 constexpr int kMinPlaces = 2;       // shortest run
