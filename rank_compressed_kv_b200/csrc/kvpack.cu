@@ -506,7 +506,8 @@ kvpack_status launch_paged_attend(const kvpack_paged_dims *d, int32_t n_layers, 
     // warps per row: so many that each has about four parts
     const long long parts = pl.slots / pl.units + 1;
     cudaError_t e;
-    if (parts > 16) e = launch_pdl(pg::join_kernel<8>, (int)rows, 256, 0, st, p, rows);
+    if (parts > 64) e = launch_pdl(pg::join_kernel<32>, (int)rows, 1024, 0, st, p, rows);
+    else if (parts > 16) e = launch_pdl(pg::join_kernel<8>, (int)rows, 256, 0, st, p, rows);
     else if (parts > 8) e = launch_pdl(pg::join_kernel<4>, (int)((rows + 1) / 2), 256, 0, st, p, rows);
     else if (parts > 4) e = launch_pdl(pg::join_kernel<2>, (int)((rows + 3) / 4), 256, 0, st, p, rows);
     else {

@@ -494,11 +494,14 @@ __global__ void __launch_bounds__(32) short_kernel(const __grid_constant__ Param
 // and the rows of sequences without tokens (out 0, lse -inf).  JW warps take a row (unit, query head),
 // and with JW = 1 a warp takes rows in turn.  Where a unit's parts are follows from the lengths: the
 // sums over them are taken while the attention still runs.
+constexpr int join_warps(int JW) { return JW > 8 ? JW : 8; }         // of a block
+
 template <int JW>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p, long long rows) {
+__global__ void __launch_bounds__(join_warps(JW) * 32) join_kernel(const __grid_constant__ Params p, long long rows) {
     constexpr int kAhead = 4;                            // parts a warp loads at a time
-    __shared__ float4 red[JW > 1 ? 8 : 1][32];
-    __shared__ float ml[8][2];
+    constexpr int kRows = join_warps(JW) / JW;           // rows of a block
+    __shared__ float4 red[JW > 1 ? join_warps(JW) : 1][32];
+    __shared__ float ml[join_warps(JW)][2];
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, jw = warp % JW;
     const int LK = p.layers * p.n_kv;
@@ -506,8 +509,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
     const Lengths lens(p, lane);
     const Runs runs(lens.total > 0 ? lens.total * LK : 1, p.slots);
     bool waited = false;
-    for (long long row = (long long)blockIdx.x * (8 / JW) + warp / JW; row < rows || (JW > 1 && !waited);
-         row += (long long)gridDim.x * (8 / JW)) {
+    for (long long row = (long long)blockIdx.x * kRows + warp / JW; row < rows || (JW > 1 && !waited);
+         row += (long long)gridDim.x * kRows) {
         const bool in = row < rows;
         const long long unit = quotient(in ? row : 0, p.per_kv), lb = quotient(unit, p.n_kv);
         const int hh = (int)(row - unit * p.per_kv);
