@@ -426,7 +426,7 @@ struct PagedPlan {
 // Three forms, by the number of units and the tables' capacity (the lengths are on the device).  Measured, bf16, us:
 //   a cluster of blocks per unit, one wave of blocks      few units, caches of up to kUnitTiles tiles a warp
 //     1 x 1024 tokens (8 units) 5.3, runs 7.0; 32 x 1024 (256 units) 24.7, 30.6; ragged up to 2048: 31.9, 32.2
-//   a warp per unit                                       enough units for every warp, up to kShortTiles tiles
+//   a warp per unit                                       units for 85 % of the warps, up to kShortTiles tiles
 //     1024 units of 16 tokens 4.3, runs 13; of 512 45, 59; of 1024 85, 99; ragged up to 1024: 65, 62
 //     also few tiles on units past one wave of clusters: 512 units of 64 tokens 6.9, 11.5
 //   even runs over all units, joined                      the rest: one long sequence keeps every warp busy

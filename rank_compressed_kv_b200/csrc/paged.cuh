@@ -15,9 +15,9 @@
 // so repeated calls give equal bits.
 //
 // Measured (one B200, device time in a graph; a plain copy runs at 6549 GB/s, a read-only kernel at 7240):
-//   64 x 704 tokens, 32 KV heads, 739 MB         112 us   6616 GB/s   (short_kernel)
-//   4 x 66560 tokens, 8 KV heads, 1.09 GB        172 us   6280 GB/s   (attend_kernel + join_kernel)
-//   32 ragged sequences up to 2561, 8 KV heads    36 us   4755 GB/s   (the same: 6 us of launches, ramp and join)
+//   64 x 704 tokens, 32 KV heads, 739 MB         112 us   6600 GB/s   (short_kernel)
+//   4 x 66560 tokens, 8 KV heads, 1.09 GB        167 us   6530 GB/s   (attend_kernel + join_kernel)
+//   32 ragged sequences up to 2561, 8 KV heads    37 us   4660 GB/s   (the same: 6 us of launches, ramp and join)
 //   1 x 608 tokens, 32 KV heads, 10 MB           5.5 us               (unit_kernel: four dependent loads and a barrier)
 #pragma once
 
@@ -367,9 +367,10 @@ struct Lengths {
     }
 };
 
-// A block is one warp and takes one run; the runs fill the GPU once.  SMs do not get equal parts of the
-// memory's bandwidth, so the last warp ends 10 to 15 % after the median; shorter runs that go where an SM is
-// done even that out, but each end of a run costs about a tile and they gain nothing.
+// A block is one warp and takes one run; the runs fill the GPU once, seven an SM (eight: 4 x 66560 tokens
+// 174 us instead of 167, 16 ragged sequences of 4 layers 84 instead of 82).  SMs do not get equal parts of
+// the memory's bandwidth, so the last warp ends 10 to 15 % after the median; shorter runs that go where an SM
+// is done even that out, but each end of a run costs about a tile and they gain nothing.
 __global__ void __launch_bounds__(32) attend_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(128) unsigned char smem[];
     // in this order: the join may then read the lengths, which a kernel before this one may write
