@@ -367,7 +367,8 @@ kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, cons
  * that none of them appends to.  Lengths and tables are read on the device, so a captured
  * graph may be replayed after they have changed.  A length or a page number out of range
  * is reported as KVPACK_ERR_PAGE by kvpack_last_device_status(); nothing outside the
- * pools is touched, but that call's results are not to be used.
+ * pools is touched, but that call's results are not to be used.  CUDA loads a kernel at
+ * its first use: make one call of a shape before capturing it.
  * Supported: head_dim 128, n_q_heads a multiple of n_kv_heads with a ratio up to 8,
  * n_kv_heads <= 1024, page_size a power of two 16 .. 256, batch <= KVPACK_MAX_PAGED_BATCH,
  * max_pages * page_size <= KVPACK_MAX_PAGED_TOKENS.
