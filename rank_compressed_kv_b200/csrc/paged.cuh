@@ -72,6 +72,17 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
+// x, y >= 0 as three pairs of bf16 that sum to x and y exactly: the upper eight bits of the value, of what that
+// leaves, and the rest.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&w)[3]) {
+    #pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        w[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+        x -= __uint_as_float(w[i] << 16);
+        y -= __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
 // The softmax state of a run's current unit, as the matrix instructions lay it out.  Lane 4 g + t:
 // m, l of heads 2t, 2t + 1; o[c / 2][2 (c % 2) + e]: entry 8 c + g of head 2t + e (c < 16).
 struct State {
@@ -131,8 +142,11 @@ constexpr int kRingBytes = kSlots * kTileBytes;          // of a warp
 // whether it still belongs to the walk.  done(cu, ends, state) is called at the end of a unit (ends) or
 // of the walk, and the state starts afresh.
 //   S (16 tokens x 8 heads) = K q^T,   O^T (128 x 8 heads) += V^T P      (mma.sync, fp32 sums)
-// P goes in as bf16 hi + lo (two products): rounding it to bf16 once would add as much error as the
-// rounding of the output.  Rows past the sequence's end are not read; the copy writes zeros.
+// P goes in whole, as three bf16 terms: of two, 16 bits, values that nearly cancel leave what those lack.  The
+// matrix instruction cuts its sums off instead of rounding them, so it adds up one tile alone, and the running
+// sum takes the tile with a rounded fma: over 4 x 66560 tokens 0.05 % of the outputs are then not the nearest bf16,
+// 0.25 % with sums that stay in the accumulators.  Both cost the short caches 2 % (64 x 704: 112 to 114 us), the
+// long ones nothing.  Rows past the sequence's end are not read; the copy writes zeros.
 // Loads are asynchronous copies of 512 contiguous bytes a warp (two rows): register loads in the
 // operand layout of K, 64 bytes of each of eight rows, stream 3 % slower (6949 against 7162 GB/s over
 // 1.09 GB, loads alone).  Three slots: two tiles on their way, 128 KB an SM, more than the 56 KB that its
@@ -254,20 +268,33 @@ __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Curso
         st.l[1] = st.l[1] * f1 + (p1 + p3);
         st.m[0] = mn0;
         st.m[1] = mn1;
-        uint32_t h0, h1, q0, q1;
-        split2(p0, p1, h0, q0);
-        split2(p2, p3, h1, q1);
-        h0 = movmatrix_t(h0);
-        h1 = movmatrix_t(h1);
-        q0 = movmatrix_t(q0);
-        q1 = movmatrix_t(q1);
+        uint32_t w0[3], w1[3];
+        split3(p0, p1, w0);
+        split3(p2, p3, w1);
         #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            st.o[e][0] *= f0; st.o[e][1] *= f1; st.o[e][2] *= f0; st.o[e][3] *= f1;
-            uint32_t a[4];
-            ldsm_x4_t(tb + vrow + (((2 * e) ^ vx) << 4), a[0], a[1], a[2], a[3]);
-            mma_bf16(st.o[e], a, h0, h1);
-            mma_bf16(st.o[e], a, q0, q1);
+        for (int i = 0; i < 3; ++i) {
+            w0[i] = movmatrix_t(w0[i]);
+            w1[i] = movmatrix_t(w1[i]);
+        }
+        // two accumulators' products side by side: each is a chain of three
+        #pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float d[2][4] = {};
+            uint32_t a[2][4];
+            #pragma unroll
+            for (int k = 0; k < 2; ++k)
+                ldsm_x4_t(tb + vrow + (((2 * (e + k)) ^ vx) << 4), a[k][0], a[k][1], a[k][2], a[k][3]);
+            #pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                mma_bf16(d[0], a[0], w0[i], w1[i]);
+                mma_bf16(d[1], a[1], w0[i], w1[i]);
+            }
+            #pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float (&o)[4] = st.o[e + k];
+                o[0] = fmaf(o[0], f0, d[k][0]); o[1] = fmaf(o[1], f1, d[k][1]);
+                o[2] = fmaf(o[2], f0, d[k][2]); o[3] = fmaf(o[3], f1, d[k][3]);
+            }
         }
         --ahead;
         const bool ends = cu.t + 1 == cu.nt;             // the unit ends with this tile
