@@ -72,15 +72,19 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-// x, y >= 0 as three pairs of bf16 that sum to x and y exactly: the upper eight bits of the value, of what that
-// leaves, and the rest.
+// x, y >= 0 as three pairs of bf16 that sum to x and y: the upper eight bits of the value, of what that leaves, and
+// the rest.  With their lowest bits set (2^-23 of the value at most) no term of a value from 2^-102 on is zero, and
+// none is negative: times an infinite V each gives the infinity that the whole gives, and not a NaN.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&w)[3]) {
+    x = __uint_as_float(__float_as_uint(x) | 1u);
+    y = __uint_as_float(__float_as_uint(y) | 1u);
     #pragma unroll
     for (int i = 0; i < 3; ++i) {
         w[i] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
         x -= __uint_as_float(w[i] << 16);
         y -= __uint_as_float(w[i] & 0xffff0000u);
     }
+    w[2] |= 0x00010001u;
 }
 
 // The softmax state of a run's current unit, as the matrix instructions lay it out.  Lane 4 g + t:

@@ -1,4 +1,4 @@
-"""The value product of the paged attention, against fp64: values that nearly cancel, and long sums."""
+"""The value product of the paged attention, against fp64: values that nearly cancel, long sums, and infinite values."""
 import math
 
 import pytest
@@ -95,3 +95,85 @@ def test_sums_over_many_tiles_are_rounded_and_not_cut_off():
     got = out.double()[..., 5]
     assert bool(((got - want).abs() <= tol + 2.0 ** -8 * want).all()), (got, want, tol)
     assert float((lse.double() - math.log(length)).abs().max()) <= 2.0 ** -20 * math.log(length)
+
+
+@pytest.mark.parametrize("batch,wide", FORMS)
+def test_infinite_values_follow_the_formula(batch, wide):
+    """An infinite value of a weight above 0 makes its entry infinite, infinities of both signs, a NaN value and an infinite
+    one of weight 0 (a logit of -inf) make theirs NaN; all other entries are as they are without them."""
+    import rank_compressed_kv_b200 as kv
+    page, n_kv = 16, 4
+    length = 60 if wide == 0 else 700
+    g = torch.Generator().manual_seed(4)
+    table, n_pages = pages_for([length] * batch, page, g, wide=wide)
+    K, V = normal(g, 1, n_pages, n_kv, page, D), normal(g, 1, n_pages, n_kv, page, D)
+    q = normal(g, batch, 2 * n_kv, D)
+    lens = [length] * batch
+    clean, clean_lse = _run(kv, lens, 2 * n_kv, n_kv, page, q, K, V, table, 0.3)
+    want = clean.clone()
+
+    def put(X, b, j, t, e, value):
+        X[0, int(table[b, t // page]), j, t % page, e] = value
+
+    for b in range(0, batch, 3):
+        for t in range(length):                                    # the entries 0 and 1: every token, the last among them
+            put(V, b, 0, t, 0, math.inf)
+            put(V, b, 0, t, 1, -math.inf)
+        want[b, :2, 0], want[b, :2, 1] = math.inf, -math.inf
+        for e, t in ((2, 0), (3, length // 2), (4, length - 1), (100, 17)):
+            put(V, b, 1, t, e, -math.inf)
+            want[b, 2:4, e] = -math.inf
+        put(V, b, 2, 5, 50, math.inf)
+        put(V, b, 2, length - 2, 50, -math.inf)
+        put(V, b, 2, 9, 51, math.nan)
+        want[b, 4:6, 50:52] = math.nan
+    out, lse = _run(kv, lens, 2 * n_kv, n_kv, page, q, K, V, table, 0.3)
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out[~torch.isnan(want)], want[~torch.isnan(want)])
+    assert torch.equal(lse, clean_lse)
+    # a weight of 0: 0 times infinity
+    q[..., 0] = 1.0
+    put(K, 0, 3, 20, 0, -math.inf)
+    put(V, 0, 3, 20, 60, math.inf)
+    out, _ = _run(kv, lens, 2 * n_kv, n_kv, page, q, K, V, table, 0.3)
+    assert bool(torch.isnan(out[0, 6:8, 60]).all()) and not bool(torch.isnan(out[0, 6:8, :60]).any())
+
+
+def test_infinite_text_values_in_the_decode_step():
+    """The decode over a paged tail gives an infinite text value's entry what it gives over the dense tail."""
+    import rank_compressed_kv_b200 as kv
+    import synth
+    from gpu_util import bf, u32
+    from synth import cases
+    n_q, n_kv, T, L = 16, 8, 200, 90
+    w = synth.Workload("paged", 7, 2, 1, n_q, n_kv, T, L, 1, "lowrank32")
+    c = cases.decode_case(w, n_layers=1, T=T, Lcap=L)
+    g = {k: bf(c[k]) for k in ("q", "CK_lo", "CK_hi", "BK", "CV_lo", "CV_hi", "BV", "K_text", "V_text")}
+    Vt = g["V_text"].view(2, n_kv // 4, L, 4, D)
+    Vt[0, 0, 3, 1, 7], Vt[0, 1, 89, 2, 127], Vt[1, 1, :, 3, 64] = math.inf, -math.inf, math.inf
+    page = 32
+    table, n_pages = pages_for([L, L], page, torch.Generator().manual_seed(2))
+    K, V = (torch.zeros(1, n_pages, n_kv, page, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    t = torch.arange(L)
+    for b in range(2):
+        at = table[b][t // page].long(), t % page
+        for X, x in ((K, g["K_text"].view(2, n_kv // 4, L, 4, D)), (V, Vt)):
+            X[0, at[0].to(DEV), :, at[1].to(DEV)] = x[b].transpose(0, 1).reshape(L, n_kv, D)
+    outs = []
+    for paged in (True, False):
+        dims = kv.Dims(batch=2, n_q_heads=n_q, n_kv_heads=n_kv, T_vis=T, L_text_cap=L)
+        pd = kv.PagedDims(2, n_q, n_kv, page, n_pages, table.shape[1])
+        out, mass = torch.empty(2, n_q, D, dtype=torch.bfloat16, device=DEV), torch.empty(dims.units(1), T, device=DEV)
+        args = [g[k] for k in ("q", "CK_lo", "CK_hi", "BK", "CV_lo", "CV_hi", "BV")]
+        if paged:
+            ws = torch.empty(kv.decode_paged_workspace(dims, pd, 1), dtype=torch.uint8, device=DEV)
+            kv.decode_attn_paged(dims, pd, 1, *args, K, V, table.to(DEV), torch.tensor([L, L], dtype=torch.int32, device=DEV),
+                                 u32(c["mask"]), 1.0, out, mass, ws)
+        else:
+            ws = torch.empty(kv.decode_workspace(dims, 1), dtype=torch.uint8, device=DEV)
+            kv.decode_attn(dims, 1, *args, g["K_text"], g["V_text"], L, u32(c["mask"]), 1.0, out, mass, ws)
+        assert kv.last_device_status() == 0
+        outs.append(out.float().cpu())
+    for value in (math.inf, -math.inf):
+        assert torch.equal(outs[0] == value, outs[1] == value)
+    assert not bool(torch.isnan(outs[0]).any()) and int(torch.isinf(outs[0]).sum()) == 6     # three entries, two heads each
