@@ -17,7 +17,7 @@ _CALL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_call.so"
 if not os.path.exists(_CALL_PATH):
     raise ImportError(f"_call.so not found at {_CALL_PATH}; build it with `python rank_compressed_kv_b200/build.py`")
 
-from ._call import paged_append, paged_decode_attn, rope  # noqa: E402, F401
+from ._call import paged_append, paged_decode_attn, rope, structures  # noqa: E402, F401
 
 
 class _CRopeSpec(ctypes.Structure):
@@ -62,7 +62,10 @@ class Rope:
             raise ValueError(f"{n} pairs need an axis each, below {n_axes}")
         self.rotary_dim, self.n_axes, self.axis_of_pair, self.adjacent = rotary_dim, n_axes, axis_of_pair, bool(adjacent)
         self._c = _CRopeSpec(rotary_dim, n_axes, int(self.adjacent), (ctypes.c_uint8 * 64)(*axis_of_pair))
-        self._at = ctypes.addressof(self._c)          # what the extension reads; lives as long as this object
+
+    @property
+    def _at(self):
+        return ctypes.addressof(self._c)              # of this object's own structure, in copies too
 
     def frequencies(self, theta: float = 10000.0, device="cuda"):
         """theta^(-2p / rotary_dim) of each pair p: float64, the freq argument of rope and paged_append."""
@@ -84,23 +87,36 @@ class PagedDims:
         c = _CPagedDims(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
                         self.max_pages)
         object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_at", ctypes.addressof(c))
+
+    @property
+    def _at(self):
+        return ctypes.addressof(self._c)              # of this object's own structure, in copies too
 
     def c(self) -> _CPagedDims:
         return self._c
 
 
+structures(_CRopeSpec, _CPagedDims)
+
+
+def _dims_at(dims) -> int:
+    if not isinstance(dims, PagedDims):
+        raise TypeError(f"{type(dims).__name__} is not a PagedDims")
+    return dims._at
+
+
 def paged_decode_workspace(dims: PagedDims, n_layers: int) -> int:
-    return int(_L.kvpack_paged_decode_workspace(dims._at, n_layers))
+    return int(_L.kvpack_paged_decode_workspace(_dims_at(dims), n_layers))
 
 
 def decode_paged_workspace(dims: Dims, pdims: PagedDims, n_layers: int) -> int:
-    return int(_L.kvpack_decode_paged_workspace(ctypes.byref(dims.c()), pdims._at, n_layers))
+    return int(_L.kvpack_decode_paged_workspace(ctypes.byref(dims.c()), _dims_at(pdims), n_layers))
 
 
 def decode_attn_paged(dims: Dims, pdims: PagedDims, n_layers: int, q, CK_lo, CK_hi, BK, CV_lo, CV_hi, BV, K_pages,
                       V_pages, block_table, seq_lens, mask, scale: float, out, mass, ws, stream=None):
     """decode_attn with the text tail in pages: batch row b has seq_lens[b] text tokens."""
+    at = _dims_at(pdims)
     pool = (n_layers, pdims.n_pages, pdims.n_kv_heads, pdims.page_size, pdims.head_dim)
     for t, what, dtype, shape in ((K_pages, "K_pages", torch.bfloat16, pool), (V_pages, "V_pages", torch.bfloat16, pool),
                                   (block_table, "block_table", torch.int32, (pdims.batch, pdims.max_pages)),
@@ -111,7 +127,7 @@ def decode_attn_paged(dims: Dims, pdims: PagedDims, n_layers: int, q, CK_lo, CK_
             raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
         if not t.is_cuda or t.get_device() != torch.cuda.current_device():
             raise ValueError(f"{what} is not on the current CUDA device")
-    _check(_L.kvpack_decode_attn_paged(ctypes.byref(dims.c()), pdims._at, n_layers, _ptr(q), _ptr(CK_lo), _ptr(CK_hi),
+    _check(_L.kvpack_decode_attn_paged(ctypes.byref(dims.c()), at, n_layers, _ptr(q), _ptr(CK_lo), _ptr(CK_hi),
                                        _ptr(BK), _ptr(CV_lo), _ptr(CV_hi), _ptr(BV), _ptr(K_pages), _ptr(V_pages),
                                        _ptr(block_table), _ptr(seq_lens), _ptr(mask), float(scale), _ptr(out),
                                        _ptr(mass), _ptr(ws), _nbytes(ws), _stream(stream)), "kvpack_decode_attn_paged")

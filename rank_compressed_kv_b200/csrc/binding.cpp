@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <stdexcept>
 #include <string>
 
@@ -65,23 +66,42 @@ int64_t integer(PyObject *o, const char *what) {
     return v;
 }
 
-// The C structure behind a Rope or PagedDims object (its attribute _at)
-PyObject *g_at = nullptr, *g_cuda_stream = nullptr;
+// The C structure of a Rope or PagedDims object, which its attribute _c holds as a ctypes structure of the type that
+// structures() was given: copied out, so that nothing here follows an address that an object carries.
+PyObject *g_c = nullptr, *g_cuda_stream = nullptr;
+PyObject *g_spec_type = nullptr, *g_dims_type = nullptr;
 
 template <typename T>
-const T *structure(PyObject *o, const char *what) {
-    PyObject *a = PyObject_GetAttr(o, g_at);
-    if (a == nullptr) {
+T structure(PyObject *o, PyObject *type, const char *what) {
+    T v;
+    PyObject *c = PyObject_GetAttr(o, g_c);
+    Py_buffer b;
+    bool ok = c != nullptr && type != nullptr && PyObject_TypeCheck(c, reinterpret_cast<PyTypeObject *>(type)) &&
+              PyObject_GetBuffer(c, &b, PyBUF_SIMPLE) == 0;
+    if (ok) {
+        ok = b.len == (Py_ssize_t)sizeof(T);
+        if (ok) std::memcpy(&v, b.buf, sizeof(T));
+        PyBuffer_Release(&b);
+    }
+    Py_XDECREF(c);
+    if (!ok) {
         PyErr_Clear();
         throw BadCall(what);
     }
-    void *p = PyLong_AsVoidPtr(a);
-    Py_DECREF(a);
-    if (p == nullptr) {
-        PyErr_Clear();
-        throw BadCall(what);
-    }
-    return static_cast<const T *>(p);
+    return v;
+}
+
+kvpack_rope_spec rope_spec(PyObject *o) { return structure<kvpack_rope_spec>(o, g_spec_type, "spec is not a Rope"); }
+kvpack_paged_dims paged_dims(PyObject *o) { return structure<kvpack_paged_dims>(o, g_dims_type, "dims is not a PagedDims"); }
+
+PyObject *set_structures(PyObject *, PyObject *args) {
+    PyObject *spec, *dims;
+    if (!PyArg_ParseTuple(args, "O!O!", &PyType_Type, &spec, &PyType_Type, &dims)) return nullptr;
+    Py_INCREF(spec);
+    Py_INCREF(dims);
+    Py_XSETREF(g_spec_type, spec);
+    Py_XSETREF(g_dims_type, dims);
+    Py_RETURN_NONE;
 }
 
 // --------------------------------------------------------------------------------- tensors
@@ -221,19 +241,19 @@ PyObject *call_rope(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObjec
     return guarded([&]() -> PyObject * {
         PyObject *a[9];
         rope_sig.parse(args, nargs, kw, a);
-        const kvpack_rope_spec *spec = structure<kvpack_rope_spec>(a[0], "spec is not a Rope");
+        const kvpack_rope_spec spec = rope_spec(a[0]);
         const bool has_q = !none(a[3]), has_k = !none(a[5]);
         if (has_q != !none(a[4]) || has_k != !none(a[6]) || (!has_q && !has_k))
             throw Refused("an input and its output, of q, of k or of both");
         Call c;
         const at::Tensor &pos = c.tensor(a[2], "pos");
         const auto ps = pos.sizes();
-        if ((ps.size() != 2 && ps.size() != 3) || ps[0] != spec->n_axes)
-            throw Refused("pos has shape " + Call::shape_of(ps) + ": [" + std::to_string(spec->n_axes) +
+        if ((ps.size() != 2 && ps.size() != 3) || ps[0] != spec.n_axes)
+            throw Refused("pos has shape " + Call::shape_of(ps) + ": [" + std::to_string(spec.n_axes) +
                           "][batch][T] is wanted");
         const int64_t outer = ps.size() == 3 ? ps[1] : 1, rows = ps.back();
         const void *pp = c.dense(a[2], "pos", at::kInt, ps);
-        const void *fp = c.dense(a[1], "freq", at::kDouble, {spec->rotary_dim / 2});
+        const void *fp = c.dense(a[1], "freq", at::kDouble, {spec.rotary_dim / 2});
         kvpack_heads q{}, qo{}, k{}, ko{};
         int64_t n_q = 0, n_k = 0;
         if (has_q) {
@@ -254,7 +274,7 @@ PyObject *call_rope(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObjec
         void *st = c.stream(a[8]);
         int s;
         Py_BEGIN_ALLOW_THREADS
-        s = kvpack_rope(spec, static_cast<const double *>(fp), static_cast<const int32_t *>(pp), (int32_t)outer,
+        s = kvpack_rope(&spec, static_cast<const double *>(fp), static_cast<const int32_t *>(pp), (int32_t)outer,
                         (int32_t)rows, (int32_t)n_q, &q, &qo, (int32_t)n_k, &k, &ko, inverse, st);
         Py_END_ALLOW_THREADS
         return finish(s, "kvpack_rope");
@@ -291,7 +311,7 @@ PyObject *call_append(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObj
     return guarded([&]() -> PyObject * {
         PyObject *a[15];
         append_sig.parse(args, nargs, kw, a);
-        const kvpack_paged_dims *d = structure<kvpack_paged_dims>(a[0], "dims is not a PagedDims");
+        const kvpack_paged_dims dims = paged_dims(a[0]), *d = &dims;
         const int64_t layers = integer(a[1], "n_layers");
         Call c;
         const at::Tensor &kt = c.tensor(a[6], "k");
@@ -309,9 +329,11 @@ PyObject *call_append(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObj
         }
         const Pool p = pool(c, d, layers, a[12], a[13], a[10], a[9]);
         const void *off = none(a[8]) ? nullptr : c.dense(a[8], "row_offsets", at::kInt, {d->batch + 1});
-        const kvpack_rope_spec *spec = none(a[2]) ? nullptr : structure<kvpack_rope_spec>(a[2], "spec is not a Rope");
+        kvpack_rope_spec rotation, *spec = nullptr;
         const void *fp = nullptr, *pp = nullptr;
-        if (spec != nullptr) {
+        if (!none(a[2])) {
+            rotation = rope_spec(a[2]);
+            spec = &rotation;
             fp = c.dense(a[3], "freq", at::kDouble, {spec->rotary_dim / 2});
             pp = c.dense(a[4], "pos", at::kInt, {spec->n_axes, rows});
         }
@@ -342,7 +364,7 @@ PyObject *call_attend(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObj
     return guarded([&]() -> PyObject * {
         PyObject *a[12];
         attend_sig.parse(args, nargs, kw, a);
-        const kvpack_paged_dims *d = structure<kvpack_paged_dims>(a[0], "dims is not a PagedDims");
+        const kvpack_paged_dims dims = paged_dims(a[0]), *d = &dims;
         const int64_t layers = integer(a[1], "n_layers"), rows = layers * d->batch;
         const double scale = PyFloat_AsDouble(a[7]);
         if (scale == -1.0 && PyErr_Occurred()) throw PyFailed();
@@ -367,6 +389,8 @@ PyObject *call_attend(PyObject *, PyObject *const *args, Py_ssize_t nargs, PyObj
 }
 
 PyMethodDef methods[] = {
+    {"structures", set_structures, METH_VARARGS,
+     "structures(spec_type, dims_type)\n--\n\nThe ctypes structures that Rope and PagedDims objects hold as _c."},
     {"rope", (PyCFunction)(void (*)(void))call_rope, METH_FASTCALL | METH_KEYWORDS, rope_doc},
     {"paged_append", (PyCFunction)(void (*)(void))call_append, METH_FASTCALL | METH_KEYWORDS, append_doc},
     {"paged_decode_attn", (PyCFunction)(void (*)(void))call_attend, METH_FASTCALL | METH_KEYWORDS, attend_doc},
@@ -378,7 +402,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", "Native argument marshalli
 }  // namespace
 
 PyMODINIT_FUNC PyInit__call(void) {
-    g_at = PyUnicode_InternFromString("_at");
+    g_c = PyUnicode_InternFromString("_c");
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     rope_sig.intern();
     append_sig.intern();
