@@ -42,7 +42,7 @@ class Rope:
 
     axis_of_pair gives the axis of each of the rotary_dim / 2 pairs; by default sections (how many
     consecutive pairs each axis has) or, without them, pair p has axis p * n_axes // (rotary_dim / 2).
-    Pairs are (p, p + rotary_dim / 2), or with adjacent (2p, 2p + 1).
+    Pairs are (p, p + rotary_dim / 2), or with adjacent (2p, 2p + 1).  These stay as they are made.
     """
 
     def __init__(self, rotary_dim: int = 128, n_axes: int = 1, sections=None, axis_of_pair=None, adjacent: bool = False):
@@ -60,8 +60,13 @@ class Rope:
         axis_of_pair = tuple(int(a) for a in axis_of_pair)
         if len(axis_of_pair) != n or any(not 0 <= a < n_axes for a in axis_of_pair):
             raise ValueError(f"{n} pairs need an axis each, below {n_axes}")
-        self.rotary_dim, self.n_axes, self.axis_of_pair, self.adjacent = rotary_dim, n_axes, axis_of_pair, bool(adjacent)
-        self._c = _CRopeSpec(rotary_dim, n_axes, int(self.adjacent), (ctypes.c_uint8 * 64)(*axis_of_pair))
+        vars(self).update(rotary_dim=rotary_dim, n_axes=n_axes, axis_of_pair=axis_of_pair, adjacent=bool(adjacent),
+                          _c=_CRopeSpec(rotary_dim, n_axes, int(bool(adjacent)), (ctypes.c_uint8 * 64)(*axis_of_pair)))
+
+    def __setattr__(self, name, value):
+        if name in ("rotary_dim", "n_axes", "axis_of_pair", "adjacent", "_c"):
+            raise AttributeError(f"a Rope's {name} is not changed in place")   # the calls read _c, made in __init__
+        object.__setattr__(self, name, value)
 
     @property
     def _at(self):

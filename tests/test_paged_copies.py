@@ -94,3 +94,12 @@ def test_neither_is_taken_for_the_other(kv):
     with pytest.raises(TypeError, match="spec is not a Rope"):
         kv.paged_append(_dims(kv), 1, d, torch.zeros(64, dtype=torch.float64), torch.zeros(1, 3, dtype=torch.int32), None,
                         x[:, :8], x[:, :8], None, i, torch.zeros(3, 500, dtype=torch.int32), None, pool, pool)
+
+def test_a_rotation_is_not_changed_in_place(kv):
+    s = kv.Rope()
+    for name, value in (("rotary_dim", 64), ("n_axes", 2), ("adjacent", True), ("axis_of_pair", (0,) * 64)):
+        with pytest.raises(AttributeError):
+            setattr(s, name, value)
+    assert (s.rotary_dim, s.n_axes, s.adjacent) == (128, 1, False)
+    s.freq = 1                                        # other attributes are the user's own
+    assert s.freq == 1
