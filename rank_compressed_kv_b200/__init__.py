@@ -5,7 +5,8 @@ attention-aware partial decompression (AttentionPack), as sm_100a kernels
 behind a C ABI.  This module only marshals arguments: torch tensors become
 device pointers, the current torch stream becomes the cudaStream_t.  Every
 step of the computation runs in the library's CUDA kernels; there is no CPU
-path, and importing fails if libkvpack.so has not been built.
+path, and importing fails if libkvpack.so has not been built.  rope, paged_append
+and paged_decode_attn need _call.so too, built with it.
 
 Functions mirror the C entry points:
 
@@ -53,13 +54,25 @@ from ._lib import (  # noqa: F401
     selftest_bounded_wait,
     version,
 )
+from . import _paged
 from ._paged import (  # noqa: F401
     PagedDims,
     Rope,
     decode_attn_paged,
     decode_paged_workspace,
-    paged_append,
-    paged_decode_attn,
     paged_decode_workspace,
-    rope,
 )
+
+__all__ = [name for name in globals() if not name.startswith("_")] + list(_paged.NATIVE)
+
+
+def __getattr__(name):
+    """rope, paged_append and paged_decode_attn: their extension is loaded at the first use."""
+    if name not in _paged.NATIVE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(_paged, name)
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_paged.NATIVE})

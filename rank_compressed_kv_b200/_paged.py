@@ -2,22 +2,31 @@
 
 rope, paged_append and paged_decode_attn are marshalled by the native extension _call
 (csrc/binding.cpp): a step of a small batch takes a few microseconds on the GPU, less than a call
-over ctypes.  The rest goes over ctypes as in _lib.
+over ctypes.  The extension, and torch with it, is loaded when one of the three is first asked for:
+what goes over ctypes, as in _lib, needs neither.
 """
 import ctypes
 import math
 import os
 from dataclasses import dataclass
 
-import torch
-
 from ._lib import Dims, _L, _check, _dims_p, _i32, _nbytes, _ptr, _stream, _sz, _vp
 
 _CALL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_call.so")
-if not os.path.exists(_CALL_PATH):
-    raise ImportError(f"_call.so not found at {_CALL_PATH}; build it with `python rank_compressed_kv_b200/build.py`")
+NATIVE = ("rope", "paged_append", "paged_decode_attn")
 
-from ._call import paged_append, paged_decode_attn, rope, structures  # noqa: E402, F401
+
+def __getattr__(name):
+    if name not in NATIVE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    if not os.path.exists(_CALL_PATH):
+        raise ImportError(f"_call.so not found at {_CALL_PATH}; build it with `python rank_compressed_kv_b200/build.py`")
+    import torch  # noqa: F401  (its libraries, before the extension that needs them)
+
+    from . import _call
+    _call.structures(_CRopeSpec, _CPagedDims)
+    globals().update({n: getattr(_call, n) for n in NATIVE})
+    return globals()[name]
 
 
 class _CRopeSpec(ctypes.Structure):
@@ -74,6 +83,7 @@ class Rope:
 
     def frequencies(self, theta: float = 10000.0, device="cuda"):
         """theta^(-2p / rotary_dim) of each pair p: float64, the freq argument of rope and paged_append."""
+        import torch
         p = torch.arange(self.rotary_dim // 2, dtype=torch.float64, device=device)
         return theta ** (-2.0 * p / self.rotary_dim)
 
@@ -101,9 +111,6 @@ class PagedDims:
         return self._c
 
 
-structures(_CRopeSpec, _CPagedDims)
-
-
 def _dims_at(dims) -> int:
     if not isinstance(dims, PagedDims):
         raise TypeError(f"{type(dims).__name__} is not a PagedDims")
@@ -121,6 +128,7 @@ def decode_paged_workspace(dims: Dims, pdims: PagedDims, n_layers: int) -> int:
 def decode_attn_paged(dims: Dims, pdims: PagedDims, n_layers: int, q, CK_lo, CK_hi, BK, CV_lo, CV_hi, BV, K_pages,
                       V_pages, block_table, seq_lens, mask, scale: float, out, mass, ws, stream=None):
     """decode_attn with the text tail in pages: batch row b has seq_lens[b] text tokens."""
+    import torch
     at = _dims_at(pdims)
     pool = (n_layers, pdims.n_pages, pdims.n_kv_heads, pdims.page_size, pdims.head_dim)
     for t, what, dtype, shape in ((K_pages, "K_pages", torch.bfloat16, pool), (V_pages, "V_pages", torch.bfloat16, pool),
