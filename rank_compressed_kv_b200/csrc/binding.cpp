@@ -399,9 +399,31 @@ PyMethodDef methods[] = {
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", "Native argument marshalling of libkvpack's per-step calls.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 
+// The extension reads torch's and Python's own structures: one that was built for others is refused, not tried.
+bool built_for_these() {
+    const std::string python = std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION) + ".";
+    const std::string have = Py_GetVersion();
+    if (have.compare(0, python.size(), python) != 0) {
+        PyErr_Format(PyExc_ImportError, "_call.so was built for Python %sx, this is %s; run rank_compressed_kv_b200/build.py",
+                     python.c_str(), have.c_str());
+        return false;
+    }
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *version = torch != nullptr ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    Py_XDECREF(torch);
+    const char *is = version != nullptr ? PyUnicode_AsUTF8(version) : nullptr;
+    const bool same = is != nullptr && std::strcmp(is, KVPACK_TORCH) == 0;
+    if (is != nullptr && !same)
+        PyErr_Format(PyExc_ImportError, "_call.so was built for torch %s, this is %s; run rank_compressed_kv_b200/build.py",
+                     KVPACK_TORCH, is);
+    Py_XDECREF(version);
+    return same;
+}
+
 }  // namespace
 
 PyMODINIT_FUNC PyInit__call(void) {
+    if (!built_for_these()) return nullptr;
     g_c = PyUnicode_InternFromString("_c");
     g_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     rope_sig.intern();

@@ -71,3 +71,43 @@ except AttributeError:
     assert r.stdout.strip() == "done", r.stderr
     r = _python("from rank_compressed_kv_b200 import *\nprint(rope.__name__, decode_attn.__name__, PagedDims.__name__)")
     assert r.stdout.split() == ["rope", "decode_attn", "PagedDims"], r.stderr
+
+
+def _build_module():
+    import __graft_entry__
+    return __graft_entry__._build_module()
+
+
+def test_the_extension_is_rebuilt_for_another_torch_or_python(tmp_path, monkeypatch):
+    b = _build_module()
+    assert b.call_is_fresh()
+    for name in ("CALL", "CALL_FOR"):
+        shutil.copy(getattr(b, name), tmp_path)
+        monkeypatch.setattr(b, name, str(tmp_path / os.path.basename(getattr(b, name))))
+    os.utime(b.CALL)
+    assert b.call_is_fresh()
+    now, at = b.call_for(), b._torch()[0]
+    monkeypatch.setattr(b, "_torch", lambda: (at, "9.9.9"))
+    assert not b.call_is_fresh()
+    monkeypatch.undo()
+    for name in ("CALL", "CALL_FOR"):
+        monkeypatch.setattr(b, name, str(tmp_path / os.path.basename(getattr(b, name))))
+    with open(b.CALL_FOR, "w") as f:
+        f.write(now.replace("cpython-3", "cpython-2"))
+    assert not b.call_is_fresh()
+    os.remove(b.CALL_FOR)                     # one of which nothing is known
+    assert not b.call_is_fresh()
+
+
+def test_an_extension_for_another_torch_is_not_loaded():
+    r = _python("import torch\nhave = torch.__version__\ntorch.__version__ = type(have)('9.9.9')\n" + OTHERS + """
+for _ in range(2):
+    try:
+        kv.rope
+    except ImportError as e:
+        assert "built for torch " + have in str(e) and "9.9.9" in str(e), e
+    else:
+        raise AssertionError
+print("done")
+""")
+    assert r.stdout.strip() == "done", r.stderr
