@@ -130,14 +130,21 @@ def decode_attn_paged(dims: Dims, pdims: PagedDims, n_layers: int, q, CK_lo, CK_
     """decode_attn with the text tail in pages: batch row b has seq_lens[b] text tokens."""
     import torch
     at = _dims_at(pdims)
+    # the checks of paged_decode_attn: pools by their number of elements, the others by shape, devices last
     pool = (n_layers, pdims.n_pages, pdims.n_kv_heads, pdims.page_size, pdims.head_dim)
-    for t, what, dtype, shape in ((K_pages, "K_pages", torch.bfloat16, pool), (V_pages, "V_pages", torch.bfloat16, pool),
-                                  (block_table, "block_table", torch.int32, (pdims.batch, pdims.max_pages)),
-                                  (seq_lens, "seq_lens", torch.int32, (pdims.batch,))):
+    cache = ((K_pages, "K_pages", torch.bfloat16, pool), (V_pages, "V_pages", torch.bfloat16, pool),
+             (block_table, "block_table", torch.int32, (pdims.batch, pdims.max_pages)),
+             (seq_lens, "seq_lens", torch.int32, (pdims.batch,)))
+    for t, what, dtype, shape in cache:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} is not a tensor")
         if t.dtype != dtype and not (dtype == torch.bfloat16 and t.dtype == torch.int16):
             raise ValueError(f"{what} is {t.dtype}, not {dtype}")
-        if t.numel() != math.prod(shape):
+        if t.numel() != math.prod(shape) or (shape is not pool and tuple(t.shape) != shape):
             raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: kvpack takes contiguous tensors")
+    for t, what, _, _ in cache:
         if not t.is_cuda or t.get_device() != torch.cuda.current_device():
             raise ValueError(f"{what} is not on the current CUDA device")
     _check(_L.kvpack_decode_attn_paged(ctypes.byref(dims.c()), at, n_layers, _ptr(q), _ptr(CK_lo), _ptr(CK_hi),
