@@ -287,7 +287,9 @@ struct Pool {
 };
 
 Pool pool(Call &c, const kvpack_paged_dims *d, int64_t layers, PyObject *K, PyObject *V, PyObject *table, PyObject *lens) {
-    const int64_t n = layers * d->n_pages * d->n_kv_heads * d->page_size * (int64_t)d->head_dim;
+    int64_t n = layers;
+    for (int64_t f : {d->n_pages, d->n_kv_heads, d->page_size, d->head_dim})
+        if (__builtin_mul_overflow(n, f, &n)) n = INT64_MAX;             // more than any tensor has
     Pool p;
     p.K = static_cast<uint16_t *>(c.dense(K, "K_pages", at::kBFloat16, {}, n));
     p.V = static_cast<uint16_t *>(c.dense(V, "V_pages", at::kBFloat16, {}, n));

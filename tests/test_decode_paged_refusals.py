@@ -54,3 +54,14 @@ def test_other_objects_are_not_tensors(kv):
     for name in ("block_table", "seq_lens", "K_pages", "V_pages"):
         with pytest.raises(TypeError, match=f"{name} is not a tensor"):
             kv.decode_attn_paged(**{**_args(kv), name: None})
+
+
+def test_pools_whose_size_passes_64_bits(kv):
+    """8193 layers of 67100673 pages of 2^25 elements: 2^64 + 2^25, which is not 2^25."""
+    d = kv.PagedDims(batch=1, n_q_heads=1024, n_kv_heads=1024, page_size=256, n_pages=67100673, max_pages=1)
+    assert 8193 * d.n_pages * 2 ** 25 == 2 ** 64 + 2 ** 25
+    k = torch.zeros(1, 1, 1024, 128, dtype=BF).expand(8193, 1, 1024, 128)
+    pool = torch.empty(2 ** 25, dtype=BF)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="K_pages has shape"):
+        kv.paged_append(d, 8193, None, None, None, None, k, k, None, i, i[None], None, pool, pool)
