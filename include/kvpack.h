@@ -388,10 +388,11 @@ kvpack_status kvpack_rope(const kvpack_rope_spec *spec, const double *freq, cons
  *   s_t = softmax_scale * q_h . K_t[j],  t < seq_lens[b]
  *   out_h = sum_t softmax(s)_t V_t[j],   lse_h = ln sum_t exp(s_t)
  * q, out [n_layers * batch][n_q_heads][128]; lse [n_layers * batch][n_q_heads] fp32 or
- * NULL.  A sequence of length 0 gets out = 0 and lse = -inf.  Weights and sums are fp32;
- * infinities and NaN of tokens go through the formula, but an infinite V whose weight is
- * less than 2^-102 of the row's largest may give NaN.  The work split depends on the
- * shapes and lengths alone, so repeated calls give identical bits.  ws must hold kvpack_paged_decode_workspace(dims, n_layers) bytes; calls that may
+ * NULL.  A sequence of length 0 gets out = 0 and lse = -inf.  Weights and sums are fp32
+ * (values of more than 3.4e38 / length may overflow them); infinities and NaN of tokens go
+ * through the formula, but an infinite V whose weight is less than 2^-102 of the row's
+ * largest may give NaN.  The work split depends on the shapes and lengths alone, so
+ * repeated calls give identical bits.  ws must hold kvpack_paged_decode_workspace(dims, n_layers) bytes; calls that may
  * run at the same time need one each.
  *
  * kvpack_decode_attn_paged -- kvpack_decode_attn with the text tail in a paged cache, of

@@ -84,7 +84,7 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&w)[3]) {
         x -= __uint_as_float(w[i] << 16);
         y -= __uint_as_float(w[i] & 0xffff0000u);
     }
-    w[2] |= 0x00010001u;
+    w[2] |= __vminu2(w[0], 0x00010001u);                 // and none of 0 is above it
 }
 
 // The softmax state of a run's current unit, as the matrix instructions lay it out.  Lane 4 g + t:

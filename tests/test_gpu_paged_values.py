@@ -139,6 +139,28 @@ def test_infinite_values_follow_the_formula(batch, wide):
     assert bool(torch.isnan(out[0, 6:8, 60]).all()) and not bool(torch.isnan(out[0, 6:8, :60]).any())
 
 
+@pytest.mark.parametrize("batch,wide", FORMS)
+def test_weights_of_zero_take_nothing_of_the_largest_values(batch, wide):
+    """Tokens of a logit of -inf, and of one 200 below the largest (exp2 gives 0 in fp32), with values of 2e35: the largest of
+    which the sum of 700, the weights of a part that holds no others being 1, stays below fp32's largest, 3.4e38."""
+    import rank_compressed_kv_b200 as kv
+    page, n_kv = 16, 4
+    length = 60 if wide == 0 else 700
+    g = torch.Generator().manual_seed(5)
+    table, n_pages = pages_for([length] * batch, page, g, wide=wide)
+    K = torch.zeros(1, n_pages, n_kv, page, D, dtype=torch.bfloat16)
+    V = torch.full_like(K, 2e35)
+    K[..., 0] = torch.tensor([-math.inf, -200.0]).repeat(page // 2)
+    for b in range(batch):                                          # one token of weight 1
+        at = int(torch.randint(0, length, (1,), generator=g))
+        K[0, int(table[b, at // page]), :, at % page, 0] = 0
+        V[0, int(table[b, at // page]), :, at % page] = 0.25
+    q = torch.zeros(batch, 2 * n_kv, D, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    out, lse = _run(kv, [length] * batch, 2 * n_kv, n_kv, page, q, K, V, table, 1.0)
+    assert bool((out == 0.25).all()) and bool((lse == 0).all())
+
+
 def test_infinite_text_values_in_the_decode_step():
     """The decode over a paged tail gives an infinite text value's entry what it gives over the dense tail."""
     import rank_compressed_kv_b200 as kv
