@@ -425,12 +425,13 @@ struct PagedPlan {
 
 // Three forms, by the number of units and the tables' capacity (the lengths are on the device).  Measured, bf16, us:
 //   a cluster of blocks per unit, one wave of blocks      few units, caches of up to kUnitTiles tiles a warp
-//     1 x 1024 tokens (8 units) 5.3, runs 7.0; 32 x 1024 (256 units) 24.7, 30.6; ragged up to 2048: 31.9, 32.2
+//     1 x 1024 tokens (8 units) 5.3, runs 6.9; 32 x 1024 (256 units) 24.7, 29.5; ragged up to 2048: 34.4, 31.3
 //   a warp per unit                                       units for 85 % of the warps, up to kShortTiles tiles
-//     1024 units of 16 tokens 4.3, runs 13; of 512 45, 59; of 1024 85, 99; ragged up to 1024: 65, 62
-//     also few tiles on units past one wave of clusters: 512 units of 64 tokens 6.9, 11.5
+//     1024 units of 16 tokens 4.0, runs 7.5; of 512 44, 48; of 1024 83, 89; ragged up to 1024: 69, 53
+//     also few tiles on units past one wave of clusters: 512 units of 64 tokens 7.0, 11.0
 //   even runs over all units, joined                      the rest: one long sequence keeps every warp busy
-// The limits keep a long sequence among short ones, which only the runs share out, to some tens of us.
+// The limits keep a long sequence among short ones, which only the runs share out, to some tens of us.  Short
+// caches behind a table for long ones take the runs too: 1 x 64 tokens 4.1 us behind a table for 64, 6.0 for 32768.
 constexpr int kUnitTiles = 32;
 constexpr int kShortTiles = 64;
 
@@ -442,7 +443,7 @@ PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     const long long places = pl.units * ((long long)d->max_pages * d->page_size / pg::kTile + 1);
     const long long runs = (places + pg::kMinPlaces - 1) / pg::kMinPlaces;
     // as many runs for each of a few units, so that the ends of equal units are ends of runs: 4 x 66560 tokens
-    // (32 units) 166 us with 1024 runs, 174 with 1036 or, eight an SM, 1184
+    // (32 units) 165 us with 1024 runs, 171 with 1036 or, eight an SM, 1184
     long long most = (long long)kPlanSMs * pg::kSlotsPerSM;
     if (pl.units * 8 <= most) most -= most % pl.units;
     pl.slots = (int)(runs < most ? runs : most);
@@ -452,7 +453,7 @@ PagedPlan plan_paged(const kvpack_paged_dims *d, int32_t n_layers) {
     const long long warps = kPlanSMs * pg::kShortPerSM;
     if (pl.units > wave && cap <= (pl.units * 20 >= warps * 17 ? kShortTiles : 4))
         pl.shorts = (int)(pl.units < warps ? pl.units : warps);
-    // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 33.7, 28.9)
+    // past two waves of blocks the runs are level or ahead (1024 units of 256 tokens: 32.8, 27.3)
     else if (pl.units <= 2 * wave && cap <= (long long)S * pg::kWarps * kUnitTiles) pl.cluster = S;
     const size_t slots = pl.cluster > 0 || pl.shorts > 0 ? 0 : 2 * (size_t)pl.slots;
     size_t off = 0;

@@ -14,11 +14,12 @@
 // Which, goes by the shapes (launch_paged_attend's plan); how tiles are shared goes by the lengths alone,
 // so repeated calls give equal bits.
 //
-// Measured (one B200, device time in a graph; a plain copy runs at 6549 GB/s, a read-only kernel at 7240):
-//   64 x 704 tokens, 32 KV heads, 739 MB         112 us   6600 GB/s   (short_kernel)
-//   4 x 66560 tokens, 8 KV heads, 1.09 GB        167 us   6530 GB/s   (attend_kernel + join_kernel)
-//   32 ragged sequences up to 2561, 8 KV heads    37 us   4660 GB/s   (the same: 6 us of launches, ramp and join)
-//   1 x 608 tokens, 32 KV heads, 10 MB           5.5 us               (unit_kernel: four dependent loads and a barrier)
+// Measured (one B200, launches in a graph; a plain copy runs at 6549 GB/s, a read-only kernel at 7240; calls from
+// Python one behind the other take 0 to 3 us more):
+//   64 x 704 tokens, 32 KV heads, 739 MB         114 us   6480 GB/s   (short_kernel)
+//   4 x 66560 tokens, 8 KV heads, 1.09 GB        164 us   6650 GB/s   (attend_kernel + join_kernel)
+//   32 ragged sequences up to 2561, 8 KV heads    37 us   4650 GB/s   (the same: 6 us of launches, ramp and join)
+//   1 x 608 tokens, 32 KV heads, 10 MB           5.6 us               (unit_kernel: four dependent loads and a barrier)
 #pragma once
 
 #include "common.cuh"
@@ -153,8 +154,9 @@ constexpr int kRingBytes = kSlots * kTileBytes;          // of a warp
 // long ones nothing.  Rows past the sequence's end are not read; the copy writes zeros.
 // Loads are asynchronous copies of 512 contiguous bytes a warp (two rows): register loads in the
 // operand layout of K, 64 bytes of each of eight rows, stream 3 % slower (6949 against 7162 GB/s over
-// 1.09 GB, loads alone).  Three slots: two tiles on their way, 128 KB an SM, more than the 56 KB that its
-// part of the bandwidth needs at 1.2 us of latency; with two slots the whole is 20 % slower.
+// 1.09 GB, loads alone).  Three slots: two tiles on their way, 112 KB an SM with attend_kernel's seven warps and
+// 128 KB with the other kernels' eight, more than the 56 KB that its part of the bandwidth needs at 1.2 us of
+// latency; with two slots the whole is 20 % slower.
 template <typename Advance, typename Done>
 __device__ __forceinline__ void walk(const Params &p, unsigned char *ring, Cursor ld, Advance advance, Done done) {
     const int lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
@@ -399,7 +401,7 @@ struct Lengths {
 };
 
 // A block is one warp and takes one run; the runs fill the GPU once, seven an SM (eight: 4 x 66560 tokens
-// 174 us instead of 167, 16 ragged sequences of 4 layers 84 instead of 82).  SMs do not get equal parts of
+// 171 us instead of 165, ragged batches level).  SMs do not get equal parts of
 // the memory's bandwidth, so the last warp ends 10 to 15 % after the median; shorter runs that go where an SM
 // is done even that out, but each end of a run costs about a tile and they gain nothing.
 __global__ void __launch_bounds__(32) attend_kernel(const __grid_constant__ Params p) {
@@ -525,7 +527,8 @@ __global__ void __launch_bounds__(32) short_kernel(const __grid_constant__ Param
 //   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k,
 // and the rows of sequences without tokens (out 0, lse -inf).  JW warps take a row (unit, query head),
 // and with JW = 1 a warp takes rows in turn.  Where a unit's parts are follows from the lengths: the
-// sums over them are taken while the attention still runs.
+// sums over them are taken while the attention still runs.  (With 32 warps a block 64 registers a thread are
+// all there are, and 76 bytes of join_kernel<32> are spilled.)
 constexpr int join_warps(int JW) { return JW > 8 ? JW : 8; }         // of a block
 
 template <int JW>
@@ -642,7 +645,7 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t a) {
 
 // Short caches of few units: a cluster takes one unit, its warps equal shares of the unit's tiles,
 // and the parts meet in the blocks' shared memories.  One launch, nothing to scan, no workspace:
-// 1 x 608 tokens of 32 heads 5.5 us, 6.8 as runs and join.
+// 1 x 608 tokens of 32 heads 5.6 us, 7.0 as runs and join.
 __global__ void __launch_bounds__(kThreads, kUnitBlocksPerSM) unit_kernel(const __grid_constant__ Params p, int S) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float2 pml[kWarps][8];

@@ -5,7 +5,8 @@
 //   (x, y) -> (x cos t - y sin t, y cos t + x sin t),   the inverse by -t (also the gradient);
 // entries R .. 127 pass unchanged.  Angles of far positions need more than 32 bits: the number of
 // turns, pos * freq / 2 pi, is taken in fp64, its whole part dropped, and sine and cosine of what
-// is left (at most half a turn, exact to 2^-24) are fp32, as is the rotation; one rounding to bf16.
+// is left are fp32, as is the rotation; one rounding to bf16.  What is left, at most half a turn, is off by
+// 2^-26 of a turn (its rounding to fp32) and 2^-52 of all the turns: 2^-23.4 together at position 2^31 and freq 1.
 #pragma once
 
 #include "common.cuh"
@@ -101,7 +102,7 @@ __device__ __forceinline__ void turn(uint4 &a, uint4 &b, const float (&c)[8], co
 }
 
 constexpr int kThreads = 128;
-constexpr int kBlocks = 8;          // per SM: 64 registers a thread
+constexpr int kBlocks = 8;          // per SM: 64 registers a thread (four quads at a time spill 12 bytes)
 constexpr int kWarpsPerSM = kBlocks * kThreads / 32;
 
 // A warp takes a row's heads (or a share of them) four at a time: lane 8 s + c holds head s of the
